@@ -23,7 +23,9 @@ __all__ = ["UE5M3", "E4M3", "E8M0", "ROW", "COL", "TILE2D", "QTensor", "AmaxCach
            "fake_quant", "dequantize", "FakeQuantPolicy", "mxfp4_to_fp8", "quantize_local",
            "tensor_amax",
            "gemm_fprop", "gemm_dgrad", "gemm_wgrad", "gemm_fprop_q", "gemm_dgrad_q", "decode_f16", "gemm_f16", "scale_range", "check_range", "new_stats", "debug_encode",
-           "FP4Error", "library"]
+           "FP4Error", "library",
+           "ExpertPlan", "ExpertWeights", "stack_experts", "expert_sort", "expert_gather", "expert_gather_grad",
+           "expert_combine", "expert_combine_grad", "linear", "expert_linear"]
 
 
 def library() -> ctypes.CDLL:
@@ -445,3 +447,7 @@ def debug_encode(x: torch.Tensor, which: int, u16: torch.Tensor | None = None) -
     out = torch.empty(x.numel(), dtype=torch.uint8, device=x.device)
     _lib.check(lib.fp4_debug_encode(_ptr(x), _ptr(u16), x.numel(), int(which), _ptr(out), _stream()))
     return out
+
+
+from .experts import (ExpertPlan, ExpertWeights, expert_combine, expert_combine_grad, expert_gather,  # noqa: E402
+                      expert_gather_grad, expert_linear, expert_sort, linear, stack_experts)

@@ -72,6 +72,26 @@ SIGNATURES = {
     "fp4_abi_version": ([], ctypes.c_int32),
 }
 
+# include/fp4bs_experts.h
+EXPERTS_EXPORTED = [
+    "fp4_expert_sort", "fp4_expert_sort_workspace", "fp4_expert_gather", "fp4_expert_gather_grad",
+    "fp4_expert_combine", "fp4_expert_combine_grad", "fp4_linear", "fp4_expert_linear", "fp4_linear_workspace",
+]
+
+EXPERTS_SIGNATURES = {
+    "fp4_expert_sort": ([_P, _I32, _I64, _I32, _I64, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "fp4_expert_sort_workspace": ([_I64, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "fp4_expert_gather": ([_P, _I32, _I64, _I64, _I64, _P, _I32, _P, _I64, _P], ctypes.c_int),
+    "fp4_expert_gather_grad": ([_P, _I32, _I64, _I64, _I64, _P, _I32, _P, _I64, _P], ctypes.c_int),
+    "fp4_expert_combine": ([_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _I32, _P, _I64, _P], ctypes.c_int),
+    "fp4_expert_combine_grad": ([_P, _I32, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I32, _P, _I64, _P, _I64, _P],
+                                ctypes.c_int),
+    "fp4_linear": ([_P, _I32, _I64, _I64, ctypes.POINTER(Operand), _P, _I32, _I64, _P, _SZ, _P], ctypes.c_int),
+    "fp4_expert_linear": ([_P, _I32, _I64, _I64, ctypes.POINTER(Operand), _I32, _P, _P, _I32, _I64, _P, _SZ, _P],
+                          ctypes.c_int),
+    "fp4_linear_workspace": ([_I64, _I32, ctypes.POINTER(Operand), _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+}
+
 _lib = None
 
 
@@ -84,7 +104,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         raise ImportError(f"{path} is missing: build it with `python -m fp4_block_scaled_tensor_amd.build` "
                           "(the FP4 path has no CPU or PyTorch fallback)")
     lib = ctypes.CDLL(path)
-    for name, (args, res) in SIGNATURES.items():
+    for name, (args, res) in (SIGNATURES | EXPERTS_SIGNATURES).items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res

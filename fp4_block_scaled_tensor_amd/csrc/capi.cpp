@@ -7,6 +7,8 @@
 #include <cstring>
 
 #include "../../include/fp4bs.h"
+#include "../../include/fp4bs_experts.h"
+#include "experts.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -197,6 +199,101 @@ fp4_status gemm_common(const fp4_operand* a, const fp4_operand* b, float* c, int
   const hipError_t e = g.K == 0 ? fp4k::run_fill(c, 0.0f, g.M * g.N, g.stream)
                                 : (g.fmt == FP4_E8M0) ? fp4k::run_gemm_mx(g) : fp4k::run_gemm_dec16(g);
   return hip_status(e, what);
+}
+
+// ---- the mixture-of-experts operators (fp4bs_experts.h) ----
+constexpr int32_t MAX_EXPERTS = 1024;
+constexpr int64_t MAX_SLOTS = (int64_t(1) << 31) - 1;
+
+fp4_status check_slots(int64_t tokens, int32_t topk, const char* what) {
+  if (tokens < 0) return fail(FP4_EINVAL, "%s: negative size", what);
+  if (topk < 1) return fail(FP4_EINVAL, "%s: topk must be >= 1 (got %d)", what, topk);
+  if (tokens > MAX_SLOTS / topk) return fail(FP4_EUNSUPPORTED, "%s: tokens * topk must be below 2^31", what);
+  return FP4_OK;
+}
+
+fp4_status check_experts(int32_t n_experts, const char* what) {
+  if (n_experts < 1) return fail(FP4_EINVAL, "%s: n_experts must be >= 1 (got %d)", what, n_experts);
+  if (n_experts > MAX_EXPERTS)
+    return fail(FP4_EUNSUPPORTED, "%s: at most %d experts (got %d)", what, MAX_EXPERTS, n_experts);
+  return FP4_OK;
+}
+
+// One matrix of rows: non-NULL, aligned to its elements, with a stride of at least its width.
+fp4_status check_rows(const void* p, int64_t ld, int64_t width, int64_t esz, bool nonempty, const char* what,
+                      const char* name) {
+  if (ld < width) return fail(FP4_EINVAL, "%s: %s row stride (%lld) < %lld", what, name, (long long)ld, (long long)width);
+  if (!nonempty) return FP4_OK;
+  if (!p) return fail(FP4_EINVAL, "%s: %s is NULL", what, name);
+  if (!aligned(p, (size_t)esz)) return fail(FP4_EALIGN, "%s: %s is not aligned to its elements", what, name);
+  return FP4_OK;
+}
+
+fp4_status check_row_move(int32_t dtype, int64_t tokens, int64_t hidden, const int32_t* pos, int32_t topk,
+                          const char* what) {
+  if (dtype != FP4_IN_BF16 && dtype != FP4_IN_FP32) return fail(FP4_EINVAL, "%s: unknown dtype %d", what, dtype);
+  fp4_status st = check_slots(tokens, topk, what);
+  if (st != FP4_OK) return st;
+  if (hidden < 0) return fail(FP4_EINVAL, "%s: negative size", what);
+  if (hidden > (int64_t(1) << 40)) return fail(FP4_EINVAL, "%s: size too large", what);
+  if (tokens > 0 && (!pos || !aligned(pos, 4))) return fail(FP4_EINVAL, "%s: pos must be a 4-byte aligned pointer", what);
+  return FP4_OK;
+}
+
+// Fills a for a weight-only product; n_experts 0: one weight.
+fp4_status check_wlinear(const fp4_operand* w, int64_t rows, int32_t x_dtype, int32_t n_experts, const char* what,
+                         fp4k::WLinearArgs& a) {
+  fp4_status st;
+  if (x_dtype != FP4_IN_BF16 && x_dtype != FP4_IN_FP32) return fail(FP4_EINVAL, "%s: unknown input dtype %d", what, x_dtype);
+  if ((st = check_operand(w, "weight")) != FP4_OK) return st;
+  if (n_experts != 0 && (st = check_experts(n_experts, what)) != FP4_OK) return st;
+  if (rows < 0) return fail(FP4_EINVAL, "%s: negative size", what);
+  if (rows > MAX_SLOTS || w->rows > (int64_t(1) << 31) || w->k > (int64_t(1) << 31))
+    return fail(FP4_EUNSUPPORTED, "%s: rows, N and K must be below 2^31", what);
+  if (w->block == 16 && w->rows > 0 && w->k > 0 && !aligned(w->s, 4))
+    return fail(FP4_EALIGN, "%s: scales not 4-byte aligned", what);
+  a.x_f32 = x_dtype == FP4_IN_FP32;
+  a.rows = rows;
+  a.q = w->q;
+  a.s = w->s;
+  a.g = w->g;
+  a.fmt = w->fmt;
+  a.block = w->block;
+  a.layout = w->scale_layout;
+  a.g_shift = w->g_stripe ? stripe_shift(w->g_stripe) : 0;
+  a.N = w->rows;
+  a.K = w->k;
+  a.n_experts = n_experts ? n_experts : 1;
+  return FP4_OK;
+}
+
+fp4_status wlinear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx, const fp4_operand* w, int32_t n_experts,
+                   const int32_t* offsets, void* y, int32_t y_dtype, int64_t ldy, void* ws, size_t ws_bytes,
+                   void* stream, const char* what) {
+  fp4k::WLinearArgs a{};
+  fp4_status st = check_wlinear(w, rows, x_dtype, n_experts, what, a);
+  if (st != FP4_OK) return st;
+  if (y_dtype != FP4_IN_BF16 && y_dtype != FP4_IN_FP32) return fail(FP4_EINVAL, "%s: unknown output dtype %d", what, y_dtype);
+  const int64_t esz = x_dtype == FP4_IN_FP32 ? 4 : 2, osz = y_dtype == FP4_IN_FP32 ? 4 : 2;
+  if ((st = check_rows(x, ldx, w->k, esz, rows > 0 && w->k > 0, what, "x")) != FP4_OK) return st;
+  if ((st = check_rows(y, ldy, w->rows, osz, rows > 0 && w->rows > 0, what, "y")) != FP4_OK) return st;
+  if (rows > 0 && w->k > 0 && (!aligned(x, 16) || (ldx * esz) % 16))
+    return fail(FP4_EALIGN, "%s: rows of x must be 16-byte aligned", what);
+  if (n_experts != 0 && (!offsets || !aligned(offsets, 4)))
+    return fail(FP4_EINVAL, "%s: offsets must be a 4-byte aligned pointer", what);
+  a.x = x;
+  a.ldx = ldx;
+  a.y_f32 = y_dtype == FP4_IN_FP32;
+  a.y = y;
+  a.ldy = ldy;
+  a.offsets = offsets;
+  const size_t need = fp4k::wlinear_ws(a);
+  if (ws_bytes < need || (need && !ws))
+    return fail(FP4_EINVAL, "%s: workspace of %zu bytes, %zu needed", what, ws ? ws_bytes : (size_t)0, need);
+  if (need && !aligned(ws, 16)) return fail(FP4_EALIGN, "%s: workspace not 16-byte aligned", what);
+  a.ws = ws;
+  a.stream = (hipStream_t)stream;
+  return hip_status(fp4k::run_wlinear(a), what);
 }
 
 }  // namespace
@@ -585,6 +682,116 @@ fp4_status fp4_debug_encode(const float* x, const uint16_t* u16, int64_t n, int3
   if (n < 0 || which < 0 || which > 4) return fail(FP4_EINVAL, "bad n or which");
   if (n > 0 && (!x || !out || (which == 4 && !u16))) return fail(FP4_EINVAL, "NULL input/output");
   return hip_status(fp4k::run_debug_encode(x, u16, n, which, out, (hipStream_t)stream), "fp4_debug_encode");
+}
+
+fp4_status fp4_expert_sort_workspace(int64_t tokens, int32_t topk, int32_t n_experts, size_t* ws_bytes) {
+  const char* what = "fp4_expert_sort_workspace";
+  fp4_status st;
+  if ((st = check_slots(tokens, topk, what)) != FP4_OK) return st;
+  if ((st = check_experts(n_experts, what)) != FP4_OK) return st;
+  if (!ws_bytes) return fail(FP4_EINVAL, "NULL size output");
+  *ws_bytes = fp4k::expert_sort_ws(tokens * topk, n_experts);
+  return ok();
+}
+
+fp4_status fp4_expert_sort(const void* ids, int32_t ids_int64, int64_t tokens, int32_t topk, int64_t ld_ids,
+                           int32_t n_experts, int32_t* order, int32_t* pos, int32_t* offsets, void* ws,
+                           size_t ws_bytes, void* stream) {
+  const char* what = "fp4_expert_sort";
+  fp4_status st;
+  if (ids_int64 != 0 && ids_int64 != 1) return fail(FP4_EINVAL, "%s: ids_int64 must be 0 or 1", what);
+  if ((st = check_slots(tokens, topk, what)) != FP4_OK) return st;
+  if ((st = check_experts(n_experts, what)) != FP4_OK) return st;
+  if ((st = check_rows(ids, ld_ids, topk, ids_int64 ? 8 : 4, tokens > 0, what, "ids")) != FP4_OK) return st;
+  if (!offsets || !aligned(offsets, 4)) return fail(FP4_EINVAL, "%s: offsets must be a 4-byte aligned pointer", what);
+  if (tokens > 0 && (!order || !pos || !aligned(order, 4) || !aligned(pos, 4)))
+    return fail(FP4_EINVAL, "%s: order and pos must be 4-byte aligned pointers", what);
+  const size_t need = fp4k::expert_sort_ws(tokens * topk, n_experts);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 4)))
+    return fail(FP4_EINVAL, "%s: workspace of %zu bytes, %zu needed (4-byte aligned)", what, ws ? ws_bytes : (size_t)0,
+                need);
+  fp4k::SortArgs a{ids, ids_int64 != 0, tokens, ld_ids, topk, n_experts, order, pos, offsets, ws, (hipStream_t)stream};
+  return hip_status(fp4k::run_expert_sort(a), what);
+}
+
+static fp4_status row_move(const void* tok, int64_t ld_tok, const void* rows, int64_t ld_rows, int32_t dtype,
+                           int64_t tokens, int64_t hidden, const float* w, int64_t ldw, bool weighted,
+                           const int32_t* pos, int32_t topk, void* stream, bool gather, const char* what) {
+  fp4_status st;
+  if ((st = check_row_move(dtype, tokens, hidden, pos, topk, what)) != FP4_OK) return st;
+  const int64_t esz = dtype == FP4_IN_FP32 ? 4 : 2;
+  const bool some = tokens > 0 && hidden > 0;
+  if ((st = check_rows(tok, ld_tok, hidden, esz, some, what, "token rows")) != FP4_OK) return st;
+  if ((st = check_rows(rows, ld_rows, hidden, esz, some, what, "expert rows")) != FP4_OK) return st;
+  if (weighted && (st = check_rows(w, ldw, topk, 4, some, what, "weights")) != FP4_OK) return st;
+  fp4k::RowsArgs a{const_cast<void*>(tok), const_cast<void*>(rows), dtype == FP4_IN_FP32, tokens, hidden, ld_tok,
+                   ld_rows, pos, topk, w, ldw, (hipStream_t)stream};
+  return hip_status(gather ? fp4k::run_expert_gather(a) : fp4k::run_expert_join(a), what);
+}
+
+fp4_status fp4_expert_gather(const void* x, int32_t dtype, int64_t tokens, int64_t hidden, int64_t ldx,
+                             const int32_t* pos, int32_t topk, void* xs, int64_t ldxs, void* stream) {
+  return row_move(x, ldx, xs, ldxs, dtype, tokens, hidden, nullptr, 0, false, pos, topk, stream, true,
+                  "fp4_expert_gather");
+}
+
+fp4_status fp4_expert_gather_grad(const void* dxs, int32_t dtype, int64_t tokens, int64_t hidden, int64_t ldxs,
+                                  const int32_t* pos, int32_t topk, void* dx, int64_t ldx, void* stream) {
+  return row_move(dx, ldx, dxs, ldxs, dtype, tokens, hidden, nullptr, 0, false, pos, topk, stream, false,
+                  "fp4_expert_gather_grad");
+}
+
+fp4_status fp4_expert_combine(const void* ys, int32_t dtype, int64_t tokens, int64_t hidden, int64_t ldys,
+                              const float* w, int64_t ldw, const int32_t* pos, int32_t topk, void* y, int64_t ldy,
+                              void* stream) {
+  return row_move(y, ldy, ys, ldys, dtype, tokens, hidden, w, ldw, true, pos, topk, stream, false,
+                  "fp4_expert_combine");
+}
+
+fp4_status fp4_expert_combine_grad(const void* dy, int32_t dtype, int64_t tokens, int64_t hidden, int64_t lddy,
+                                   const void* ys, int64_t ldys, const float* w, int64_t ldw, const int32_t* pos,
+                                   int32_t topk, void* dys, int64_t lddys, float* dw, int64_t lddw, void* stream) {
+  const char* what = "fp4_expert_combine_grad";
+  fp4_status st;
+  if ((st = check_row_move(dtype, tokens, hidden, pos, topk, what)) != FP4_OK) return st;
+  const int64_t esz = dtype == FP4_IN_FP32 ? 4 : 2;
+  const bool some = tokens > 0 && hidden > 0;
+  if ((st = check_rows(dy, lddy, hidden, esz, some, what, "dy")) != FP4_OK) return st;
+  if (dys) {
+    if ((st = check_rows(dys, lddys, hidden, esz, some, what, "dys")) != FP4_OK) return st;
+    if ((st = check_rows(w, ldw, topk, 4, some, what, "weights")) != FP4_OK) return st;
+  }
+  if (dw) {
+    if ((st = check_rows(ys, ldys, hidden, esz, some, what, "ys")) != FP4_OK) return st;
+    if ((st = check_rows(dw, lddw, topk, 4, tokens > 0, what, "dw")) != FP4_OK) return st;
+  }
+  fp4k::CombineGradArgs a{dy, ys, dtype == FP4_IN_FP32, tokens, hidden, lddy, ldys, w, ldw, pos, topk, dys, lddys,
+                          dw, lddw, (hipStream_t)stream};
+  return hip_status(fp4k::run_expert_combine_grad(a), what);
+}
+
+fp4_status fp4_linear_workspace(int64_t rows, int32_t x_dtype, const fp4_operand* w, int32_t n_experts,
+                                size_t* ws_bytes) {
+  fp4k::WLinearArgs a{};
+  fp4_status st = check_wlinear(w, rows, x_dtype, n_experts, "fp4_linear_workspace", a);
+  if (st != FP4_OK) return st;
+  if (!ws_bytes) return fail(FP4_EINVAL, "NULL size output");
+  *ws_bytes = fp4k::wlinear_ws(a);
+  return ok();
+}
+
+fp4_status fp4_linear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx, const fp4_operand* w, void* y,
+                      int32_t y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  return wlinear(x, x_dtype, rows, ldx, w, 0, nullptr, y, y_dtype, ldy, ws, ws_bytes, stream, "fp4_linear");
+}
+
+fp4_status fp4_expert_linear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx, const fp4_operand* w,
+                             int32_t n_experts, const int32_t* offsets, void* y, int32_t y_dtype, int64_t ldy,
+                             void* ws, size_t ws_bytes, void* stream) {
+  const char* what = "fp4_expert_linear";
+  fp4_status st = check_experts(n_experts, what);
+  if (st != FP4_OK) return st;
+  return wlinear(x, x_dtype, rows, ldx, w, n_experts, offsets, y, y_dtype, ldy, ws, ws_bytes, stream, what);
 }
 
 }  // extern "C"

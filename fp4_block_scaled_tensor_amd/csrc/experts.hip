@@ -1,0 +1,456 @@
+// Mixture-of-experts data movement on gfx950: stable sort of (token, choice) slots by expert,
+// rows copied into expert order and summed back per token, and the gradients of both.
+#include "experts.hpp"
+
+namespace fp4k {
+
+namespace {
+
+// ---------------------------------------------------------------- sort
+// Stable counting sort. A wave ranks 64 consecutive slots at a time: the lanes that hold the same
+// key are found with one ballot per key bit, the rank of a lane among them is the population
+// count below it, and the wave keeps its own running position per key in LDS, so ranks follow
+// slot order and no atomic decides an order. Keys are the expert ids; a dropped slot has key E.
+constexpr int SORT_ONE_WAVES = 16;       // the one-workgroup form
+constexpr int SORT_ONE_MAX = 8192;       // slots it takes
+constexpr int SORT_WAVES = 8;            // the form with one workgroup per chunk
+constexpr int SORT_CHUNK = 2048;         // slots per chunk
+constexpr int SORT_ONE_EXPERTS = 512;    // experts it takes (16 LDS rows of E + 1 counters below 64 KiB)
+
+template <bool ID64>
+__device__ __forceinline__ uint32_t slot_key(const void* ids, int64_t ld, int topk, int64_t slot, int E) {
+  const int64_t t = slot / topk, j = slot - t * topk;
+  if constexpr (ID64) {
+    const int64_t id = reinterpret_cast<const int64_t*>(ids)[t * ld + j];
+    return id >= 0 && id < E ? (uint32_t)id : (uint32_t)E;
+  } else {
+    const int32_t id = reinterpret_cast<const int32_t*>(ids)[t * ld + j];
+    return id >= 0 && id < E ? (uint32_t)id : (uint32_t)E;
+  }
+}
+
+__device__ __forceinline__ int wave_excl_scan(int v, int lane, int& total) {
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(s, o, 64);
+    if (lane >= o) s += u;
+  }
+  total = __shfl(s, 63, 64);
+  return s - v;
+}
+
+// Exclusive scan of v over the workgroup's threads (NW waves); total in every thread.
+template <int NW>
+__device__ __forceinline__ int block_excl_scan(int v, int* part, int& total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int wt;
+  const int x = wave_excl_scan(v, lane, wt);
+  if (lane == 0) part[w] = wt;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    const int p = part[i];
+    before += i < w ? p : 0;
+    all += p;
+  }
+  __syncthreads();
+  total = all;
+  return before + x;
+}
+
+// Counts the keys of slots [lo, hi) into the wave's LDS row.
+template <bool ID64>
+__device__ __forceinline__ void wave_count(const void* ids, int64_t ld, int topk, int E, int64_t lo, int64_t hi,
+                                           int* row) {
+  for (int64_t s = lo + (threadIdx.x & 63); s < hi; s += 64) atomicAdd(&row[slot_key<ID64>(ids, ld, topk, s, E)], 1);
+}
+
+// Keeps the wave's LDS accesses in program order (the LDS itself serves a wave's accesses in order).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Places slots [lo, hi): row[key] is the wave's next position of each key.
+template <bool ID64>
+__device__ __forceinline__ void wave_place(const void* ids, int64_t ld, int topk, int E, int bits, int64_t lo,
+                                           int64_t hi, int* row, int32_t* order, int32_t* pos) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = lo; b < hi; b += 64) {
+    const int64_t s = b + lane;
+    const bool ok = s < hi;
+    const uint32_t key = ok ? slot_key<ID64>(ids, ld, topk, s, E) : 0u;
+    uint64_t same = __ballot(ok);
+    for (int i = 0; i < bits; ++i) {
+      const bool bit = (key >> i) & 1u;
+      const uint64_t m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1ull));
+    int p = 0;
+    if (ok) p = row[key] + rank;
+    wave_order();   // every lane has read its key's position before one lane of each key advances it
+    if (ok && rank == 0) row[key] = p + __popcll(same);
+    wave_order();
+    if (ok) {
+      order[p] = (int32_t)s;
+      pos[s] = key < (uint32_t)E ? p : ~p;
+    }
+  }
+}
+
+template <bool ID64>
+__global__ __launch_bounds__(SORT_ONE_WAVES * 64) void k_sort_one(const void* __restrict__ ids, int64_t ld, int topk,
+                                                                  int n, int E, int bits, int32_t* __restrict__ order,
+                                                                  int32_t* __restrict__ pos,
+                                                                  int32_t* __restrict__ offsets) {
+  extern __shared__ int rows[];   // [SORT_ONE_WAVES][E + 1]
+  __shared__ int part[SORT_ONE_WAVES];
+  const int w = threadIdx.x >> 6, keys = E + 1;
+  for (int i = threadIdx.x; i < SORT_ONE_WAVES * keys; i += SORT_ONE_WAVES * 64) rows[i] = 0;
+  __syncthreads();
+  const int seg = ((n + SORT_ONE_WAVES * 64 - 1) / (SORT_ONE_WAVES * 64)) * 64;
+  const int lo = min(n, w * seg), hi = min(n, lo + seg);
+  wave_count<ID64>(ids, ld, topk, E, lo, hi, rows + w * keys);
+  __syncthreads();
+  // thread t < E: expert t's slots over the waves, its base, then each wave's first position
+  const int t = threadIdx.x;
+  int mine = 0;
+  if (t < E)
+    for (int i = 0; i < SORT_ONE_WAVES; ++i) mine += rows[i * keys + t];
+  int kept;
+  int base = block_excl_scan<SORT_ONE_WAVES>(mine, part, kept);
+  if (t < E) {
+    offsets[t] = base;
+    for (int i = 0; i < SORT_ONE_WAVES; ++i) {
+      const int c = rows[i * keys + t];
+      rows[i * keys + t] = base;
+      base += c;
+    }
+  }
+  if (t == 0) {
+    offsets[E] = kept;
+    int b = kept;
+    for (int i = 0; i < SORT_ONE_WAVES; ++i) {
+      const int c = rows[i * keys + E];
+      rows[i * keys + E] = b;
+      b += c;
+    }
+  }
+  __syncthreads();
+  wave_place<ID64>(ids, ld, topk, E, bits, lo, hi, rows + w * keys, order, pos);
+}
+
+// counts[chunk][E + 1]
+template <bool ID64>
+__global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_count(const void* __restrict__ ids, int64_t ld, int topk,
+                                                                int n, int E, int32_t* __restrict__ counts) {
+  extern __shared__ int rows[];   // [E + 1]
+  const int keys = E + 1;
+  for (int i = threadIdx.x; i < keys; i += SORT_WAVES * 64) rows[i] = 0;
+  __syncthreads();
+  const int64_t lo = (int64_t)blockIdx.x * SORT_CHUNK, hi = min((int64_t)n, lo + SORT_CHUNK);
+  for (int64_t s = lo + threadIdx.x; s < hi; s += SORT_WAVES * 64)
+    atomicAdd(&rows[slot_key<ID64>(ids, ld, topk, s, E)], 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < keys; i += SORT_WAVES * 64) counts[(int64_t)blockIdx.x * keys + i] = rows[i];
+}
+
+// Each workgroup sums the counts of all chunks (its keys' totals) and of the chunks before its
+// own, scans the totals into the experts' offsets and places its chunk.
+template <bool ID64>
+__global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_place(const void* __restrict__ ids, int64_t ld, int topk,
+                                                                int n, int E, int bits,
+                                                                const int32_t* __restrict__ counts,
+                                                                int32_t* __restrict__ order, int32_t* __restrict__ pos,
+                                                                int32_t* __restrict__ offsets) {
+  extern __shared__ int lds[];   // total[E + 1], before[E + 1], rows[SORT_WAVES][E + 1]
+  __shared__ int part[SORT_WAVES];
+  constexpr int NTH = SORT_WAVES * 64;
+  const int keys = E + 1, w = threadIdx.x >> 6, chunk = blockIdx.x, chunks = gridDim.x;
+  int* total = lds;
+  int* before = lds + keys;
+  int* rows = lds + 2 * keys;
+  for (int i = threadIdx.x; i < (2 + SORT_WAVES) * keys; i += NTH) lds[i] = 0;
+  __syncthreads();
+  constexpr int SEG = SORT_CHUNK / SORT_WAVES;
+  const int64_t c0 = (int64_t)chunk * SORT_CHUNK;
+  const int64_t lo = min((int64_t)n, c0 + w * SEG), hi = min((int64_t)n, lo + SEG);
+  wave_count<ID64>(ids, ld, topk, E, lo, hi, rows + w * keys);
+  // the keys' columns of counts, `parts` threads to a key when there are few keys
+  const int parts = keys >= NTH ? 1 : NTH / keys;
+  if (threadIdx.x < parts * keys || keys >= NTH) {
+    const int p = keys >= NTH ? 0 : threadIdx.x / keys;
+    for (int k = keys >= NTH ? threadIdx.x : threadIdx.x - p * keys; k < keys; k += keys >= NTH ? NTH : keys) {
+      int all = 0, pre = 0;
+#pragma unroll 8
+      for (int c = p; c < chunks; c += parts) {
+        const int v = counts[(int64_t)c * keys + k];
+        all += v;
+        pre += c < chunk ? v : 0;
+      }
+      if (all) atomicAdd(&total[k], all);
+      if (pre) atomicAdd(&before[k], pre);
+    }
+  }
+  __syncthreads();
+  int kept = 0;
+  for (int k0 = 0; k0 < E; k0 += NTH) {
+    const int k = k0 + threadIdx.x;
+    int sum;
+    int base = kept + block_excl_scan<SORT_WAVES>(k < E ? total[k] : 0, part, sum);
+    kept += sum;
+    if (k < E) {
+      if (chunk == 0) offsets[k] = base;
+      base += before[k];
+      for (int i = 0; i < SORT_WAVES; ++i) {
+        const int c = rows[i * keys + k];
+        rows[i * keys + k] = base;
+        base += c;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (chunk == 0) offsets[E] = kept;
+    int b = kept + before[E];
+    for (int i = 0; i < SORT_WAVES; ++i) {
+      const int c = rows[i * keys + E];
+      rows[i * keys + E] = b;
+      b += c;
+    }
+  }
+  __syncthreads();
+  wave_place<ID64>(ids, ld, topk, E, bits, lo, hi, rows + w * keys, order, pos);
+}
+
+// ---------------------------------------------------------------- rows to and from expert order
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
+// V consecutive elements of a row as float32: 16 bytes (V = 8 bf16 or 4 float32) or one element.
+template <bool F32, bool VEC>
+struct Elems {
+  static constexpr int V = VEC ? (F32 ? 4 : 8) : 1;
+  static constexpr int ESZ = F32 ? 4 : 2;
+  static __device__ __forceinline__ v4u raw(const char* p) { return *reinterpret_cast<const v4u*>(p); }
+  static __device__ __forceinline__ void load(const char* p, float* v) {
+    if constexpr (VEC) {
+      const v4u r = raw(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) {
+          v[i] = __uint_as_float(r[i]);
+        } else {
+          v[2 * i] = bf16_lo(r[i]);
+          v[2 * i + 1] = bf16_hi(r[i]);
+        }
+      }
+    } else if constexpr (F32) {
+      v[0] = *reinterpret_cast<const float*>(p);
+    } else {
+      v[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+    }
+  }
+  static __device__ __forceinline__ void store(char* p, const float* v) {
+    if constexpr (VEC) {
+      v4u r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) r[i] = __float_as_uint(v[i]);
+        else r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+      }
+      *reinterpret_cast<v4u*>(p) = r;
+    } else if constexpr (F32) {
+      *reinterpret_cast<float*>(p) = v[0];
+    } else {
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack_bf16(v[0], 0.0f);
+    }
+  }
+};
+
+constexpr int MT = 256;   // threads of the row kernels
+
+// One token's row to its slots' rows: a plain copy (gather), or w[s] times it (gradient of the
+// combined rows).
+template <bool F32, bool VEC, bool WEIGHT>
+__global__ __launch_bounds__(MT) void k_spread(const char* __restrict__ x, int64_t ldx, int64_t hidden,
+                                               const int32_t* __restrict__ pos, int topk, int64_t n,
+                                               const float* __restrict__ w, int64_t ldw, char* __restrict__ xs,
+                                               int64_t ldxs) {
+  using E = Elems<F32, VEC>;
+  const int64_t t = blockIdx.x;
+  for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
+    float v[E::V];
+    E::load(x + (t * ldx + h) * E::ESZ, v);
+    for (int j = 0; j < topk; ++j) {
+      const int32_t p = pos[t * topk + j];
+      const int64_t row = p < 0 ? ~p : p;
+      if (row >= n) continue;
+      float o[E::V];
+      const float f = WEIGHT && p >= 0 ? w[t * ldw + j] : 1.0f;
+#pragma unroll
+      for (int i = 0; i < E::V; ++i) o[i] = p < 0 ? 0.0f : (WEIGHT ? f * v[i] : v[i]);
+      E::store(xs + (row * ldxs + h) * E::ESZ, o);
+    }
+  }
+}
+
+// A token's slots' rows summed, with weights or without.
+template <bool F32, bool VEC, bool WEIGHT>
+__global__ __launch_bounds__(MT) void k_join(const char* __restrict__ ys, int64_t ldys, int64_t hidden,
+                                             const int32_t* __restrict__ pos, int topk, int64_t n,
+                                             const float* __restrict__ w, int64_t ldw, char* __restrict__ y,
+                                             int64_t ldy) {
+  using E = Elems<F32, VEC>;
+  const int64_t t = blockIdx.x;
+  for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
+    float a[E::V];
+#pragma unroll
+    for (int i = 0; i < E::V; ++i) a[i] = 0.0f;
+    for (int j = 0; j < topk; ++j) {
+      const int32_t p = pos[t * topk + j];
+      if (p < 0 || p >= n) continue;
+      float v[E::V];
+      E::load(ys + ((int64_t)p * ldys + h) * E::ESZ, v);
+      if constexpr (WEIGHT) {
+        const float f = w[t * ldw + j];
+#pragma unroll
+        for (int i = 0; i < E::V; ++i) a[i] = __builtin_fmaf(f, v[i], a[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E::V; ++i) a[i] += v[i];
+      }
+    }
+    E::store(y + (t * ldy + h) * E::ESZ, a);
+  }
+}
+
+// dw[s] = <dy[s / topk], ys[pos[s]]>: a workgroup per slot.
+template <bool F32, bool VEC>
+__global__ __launch_bounds__(MT) void k_slot_dot(const char* __restrict__ dy, int64_t lddy,
+                                                 const char* __restrict__ ys, int64_t ldys, int64_t hidden,
+                                                 const int32_t* __restrict__ pos, int topk, int64_t n,
+                                                 float* __restrict__ dw, int64_t lddw) {
+  using E = Elems<F32, VEC>;
+  __shared__ float part[MT / 64];
+  const int64_t s = blockIdx.x, t = s / topk;
+  const int32_t p = pos[s];
+  float a = 0.0f;
+  if (p >= 0 && p < n) {
+    for (int64_t h = (int64_t)threadIdx.x * E::V; h < hidden; h += MT * E::V) {
+      float u[E::V], v[E::V];
+      E::load(dy + (t * lddy + h) * E::ESZ, u);
+      E::load(ys + ((int64_t)p * ldys + h) * E::ESZ, v);
+#pragma unroll
+      for (int i = 0; i < E::V; ++i) a = __builtin_fmaf(u[i], v[i], a);
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) a += __shfl_xor(a, o, 64);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) dw[t * lddw + (s - t * topk)] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+bool vec_ok(const void* p, int64_t ld, int64_t esz) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * esz) % 16 == 0;
+}
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// f(F32, VEC) with both as compile-time constants
+template <class F>
+void by_type(bool f32, bool vec, F&& f) {
+  if (f32) vec ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+  else vec ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
+
+dim3 row_grid(const RowsArgs& a, bool vec) {
+  const int64_t v = vec ? (a.f32 ? 4 : 8) : 1;
+  return dim3((uint32_t)a.tokens, (uint32_t)std::min<int64_t>(div_up(a.hidden, MT * v), 1024));
+}
+
+bool sort_in_one(int64_t n, int E) { return n <= SORT_ONE_MAX && E <= SORT_ONE_EXPERTS; }
+
+}  // namespace
+
+size_t expert_sort_ws(int64_t n, int E) {
+  return sort_in_one(n, E) ? 0 : (size_t)div_up(n, SORT_CHUNK) * (size_t)(E + 1) * sizeof(int32_t);
+}
+
+hipError_t run_expert_sort(const SortArgs& a) {
+  const int n = (int)(a.tokens * a.topk), E = a.n_experts;
+  int bits = 0;
+  while ((E >> bits) != 0) ++bits;   // keys 0 .. E
+  auto go = [&](auto id64) {
+    constexpr bool ID64 = decltype(id64)::value;
+    if (sort_in_one(n, E)) {
+      k_sort_one<ID64><<<1, SORT_ONE_WAVES * 64, SORT_ONE_WAVES*(E + 1) * sizeof(int), a.stream>>>(
+          a.ids, a.ld_ids, a.topk, n, E, bits, a.order, a.pos, a.offsets);
+      return;
+    }
+    const uint32_t chunks = (uint32_t)div_up(n, SORT_CHUNK);
+    int32_t* counts = reinterpret_cast<int32_t*>(a.ws);
+    k_sort_count<ID64><<<chunks, SORT_WAVES * 64, (E + 1) * sizeof(int), a.stream>>>(a.ids, a.ld_ids, a.topk, n, E,
+                                                                                    counts);
+    k_sort_place<ID64><<<chunks, SORT_WAVES * 64, (2 + SORT_WAVES) * (E + 1) * sizeof(int), a.stream>>>(
+        a.ids, a.ld_ids, a.topk, n, E, bits, counts, a.order, a.pos, a.offsets);
+  };
+  if (a.id64) go(std::true_type{});
+  else go(std::false_type{});
+  return hipGetLastError();
+}
+
+hipError_t run_expert_gather(const RowsArgs& a) {
+  if (a.tokens == 0 || a.hidden == 0) return hipSuccess;
+  const int64_t esz = a.f32 ? 4 : 2, v = a.f32 ? 4 : 8;
+  const bool vec = a.hidden % v == 0 && vec_ok(a.tok, a.ld_tok, esz) && vec_ok(a.rows, a.ld_rows, esz);
+  by_type(a.f32, vec, [&](auto f32, auto vc) {
+    k_spread<decltype(f32)::value, decltype(vc)::value, false><<<row_grid(a, vec), MT, 0, a.stream>>>(
+        (const char*)a.tok, a.ld_tok, a.hidden, a.pos, a.topk, a.tokens * a.topk, nullptr, 0, (char*)a.rows, a.ld_rows);
+  });
+  return hipGetLastError();
+}
+
+hipError_t run_expert_join(const RowsArgs& a) {
+  if (a.tokens == 0 || a.hidden == 0) return hipSuccess;
+  const int64_t esz = a.f32 ? 4 : 2, v = a.f32 ? 4 : 8;
+  const bool vec = a.hidden % v == 0 && vec_ok(a.tok, a.ld_tok, esz) && vec_ok(a.rows, a.ld_rows, esz);
+  by_type(a.f32, vec, [&](auto f32, auto vc) {
+    constexpr bool F32 = decltype(f32)::value, VEC = decltype(vc)::value;
+    if (a.w)
+      k_join<F32, VEC, true><<<row_grid(a, vec), MT, 0, a.stream>>>((const char*)a.rows, a.ld_rows, a.hidden, a.pos,
+                                                                    a.topk, a.tokens * a.topk, a.w, a.ldw,
+                                                                    (char*)a.tok, a.ld_tok);
+    else
+      k_join<F32, VEC, false><<<row_grid(a, vec), MT, 0, a.stream>>>((const char*)a.rows, a.ld_rows, a.hidden, a.pos,
+                                                                     a.topk, a.tokens * a.topk, nullptr, 0,
+                                                                     (char*)a.tok, a.ld_tok);
+  });
+  return hipGetLastError();
+}
+
+hipError_t run_expert_combine_grad(const CombineGradArgs& a) {
+  if (a.tokens == 0 || (!a.dys && !a.dw)) return hipSuccess;
+  const int64_t esz = a.f32 ? 4 : 2, v = a.f32 ? 4 : 8, n = a.tokens * a.topk;
+  const bool vec = a.hidden % v == 0 && vec_ok(a.dy, a.lddy, esz) && (!a.dw || vec_ok(a.ys, a.ldys, esz)) &&
+                   (!a.dys || vec_ok(a.dys, a.lddys, esz));
+  by_type(a.f32, vec, [&](auto f32, auto vc) {
+    constexpr bool F32 = decltype(f32)::value, VEC = decltype(vc)::value;
+    if (a.dys && a.hidden > 0) {
+      RowsArgs r{};
+      r.f32 = a.f32;
+      r.tokens = a.tokens;
+      r.hidden = a.hidden;
+      k_spread<F32, VEC, true><<<row_grid(r, vec), MT, 0, a.stream>>>((const char*)a.dy, a.lddy, a.hidden, a.pos,
+                                                                      a.topk, n, a.w, a.ldw, (char*)a.dys, a.lddys);
+    }
+    if (a.dw)
+      k_slot_dot<F32, VEC><<<(uint32_t)n, MT, 0, a.stream>>>((const char*)a.dy, a.lddy, (const char*)a.ys, a.ldys,
+                                                             a.hidden, a.pos, a.topk, n, a.dw, a.lddw);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace fp4k
