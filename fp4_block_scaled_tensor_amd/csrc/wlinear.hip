@@ -35,7 +35,8 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// this wave's copies have landed and its LDS reads are done
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
 // Orders a wave's LDS writes before its other lanes' reads (the LDS serves a wave in order).
 __device__ __forceinline__ void wave_lds_order() {
@@ -229,25 +230,27 @@ __global__ __launch_bounds__(NW * 64) void k_wlinear_rows(WParams p) {
 }
 
 // ---------------------------------------------------------------- tile form
-// A workgroup owns a BM x BN tile of one expert's outputs; WM x WN waves hold TM x TN products of
-// 32x32x16 each. K advances in steps of 64. The activation rows of a step go straight from global
-// memory into LDS; the weight's codes go through registers, are decoded there once per workgroup
-// and written to LDS as bf16. Both are double buffered: while a step is multiplied, the next step's
-// rows are in flight, its codes are decoded, and the codes of the step after it are loaded.
+// A workgroup owns a BM x 256 tile of one expert's outputs: four waves, each all BM = 32 TM rows of
+// x and 64 of the weight's rows (TM x 2 products of 32x32x16). K advances in steps of 64.
+//
+// A wave needs its weight rows for itself alone, so the codes go from global memory to registers
+// and are decoded there: lane l holds row l % 32 and, as one 16-byte load, the 32 codes of K half
+// l / 32, which feed four products (the order of k inside a step is free as long as both operands
+// agree). The rows of x, which every wave needs, go straight from global memory into LDS, double
+// buffered. Per step of a 256 x 256 tile the LDS serves 128 KiB of reads and 32 KiB of writes (1280
+// cycles at 128 bytes a cycle) against 2048 cycles of matrix products; staging the decoded weights
+// in LDS as well, with 128 x 64 outputs to a wave, took 256 KiB (2048 cycles), and was the slower
+// by the figures below.
+//
+// Fragments are read one product group ahead. The barrier of a step stands before its last group:
+// by then the step's own reads are done and the next step's rows have landed, so the next buffer's
+// first fragments load under the last group's products and the freed buffer takes the rows of the
+// step after. The next step's codes are decoded in place, group by group, behind their last use.
 //
 // An LDS row is 128 bytes (64 k); 16-byte chunk j of row r sits at position j ^ ((r >> 1) & 7), so
 // sixteen consecutive rows reading one logical chunk cover all banks.
 constexpr int BK = 64, ROWB = BK * 2;
-
-template <int WM_, int WN_, int TM_, int TN_>
-struct WTile {
-  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NW = WM * WN, NTH = NW * 64;
-  static constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
-  static constexpr int PIECES = BM / (8 * NW);      // 8-row pieces of x a wave copies per step
-  static constexpr int TASKS = BN * 2 / NTH;        // 32-code half rows a thread decodes per step
-  static constexpr int STAGE = (BM + BN) * ROWB;    // bytes of one buffer
-  static_assert(PIECES * 8 * NW == BM && TASKS * NTH == BN * 2, "tile");
-};
+constexpr int TILE_NW = 4, TILE_TN = 2, TILE_BN = TILE_NW * TILE_TN * 32;
 
 __device__ __forceinline__ uint32_t swz(int row, int chunk) { return row * ROWB + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
@@ -288,141 +291,196 @@ __device__ __forceinline__ bool find_tile(const WParams& p, int64_t mt, int& e, 
   return false;
 }
 
-template <int FMT, int B, int LAYOUT, bool YF32, class T>
-__global__ __launch_bounds__(T::NTH) void k_wlinear_tile(WParams p, int planes, int64_t plane_bytes, uint32_t mtiles,
-                                                         uint32_t ntiles) {
-  __shared__ __attribute__((aligned(1024))) char lds[2 * T::STAGE];
-  constexpr int BM = T::BM, BN = T::BN;
+struct TileArgs {
+  uint32_t mtiles, ntiles;
+  int slices;            // parts of K, each with its own output rows in `part`
+  int64_t plane_bytes;   // bytes between the bf16 parts of float32 activations
+  bool y_f32, y_vec;     // y_vec: rows of y take 4-element stores
+  float* part;           // [slices][rows][N] sums of a split K, or null: write y
+  float scale_mul;       // 2^(127 - bias) of the 3-mantissa-bit scales
+  int64_t s_row, s_k;    // scale codes: bytes between rows (16-row bands for 2D) and between blocks of K
+  int s_band;            // log2 of the rows that share a scale row (0 or 4)
+};
+
+// E8: power-of-two scales (block 32), else 3-mantissa-bit ones with block B. PLANES: bf16 parts of x.
+template <bool E8, int B, int PLANES, int TM>
+__global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(WParams p, TileArgs t) {
+  constexpr int BM = TM * 32, STAGE = BM * ROWB, TN = TILE_TN;
+  constexpr int OW = TN * 32, OLD = OW + 4;   // a wave's output columns, padded by 16 bytes
+  constexpr int OUTB = TILE_NW * 32 * OLD * 4;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE > OUTB ? 2 * STAGE : OUTB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroup ids go round-robin over the 8 dies: give each die a contiguous run of tiles, in
   // groups of 4 m-tiles that share the weight tile in its L2
-  const uint32_t total = mtiles * ntiles, per = (total + 7) / 8;
-  const uint32_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (id >= total) return;
+  const uint32_t tiles = t.mtiles * t.ntiles, total = tiles * t.slices, per = (total + 7) / 8;
+  const uint32_t all = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (all >= total) return;
+  const uint32_t slice = all / tiles, id = all - slice * tiles;
   constexpr uint32_t GM = 4;
-  const uint32_t grp = id / (GM * ntiles), gm = min(GM, mtiles - grp * GM), rest = id - grp * GM * ntiles;
-  const int64_t mt = grp * GM + rest % gm, n0 = (int64_t)(rest / gm) * BN;
+  const uint32_t grp = id / (GM * t.ntiles), gm = min(GM, t.mtiles - grp * GM), rest = id - grp * GM * t.ntiles;
+  const int64_t mt = grp * GM + rest % gm, n0 = (int64_t)(rest / gm) * TILE_BN;
   int e;
   int64_t m0, m1;
   if (!find_tile<BM>(p, mt, e, m0, m1)) return;
+  char* y = t.part ? reinterpret_cast<char*>(t.part + (int64_t)slice * p.rows * p.N) : p.y;
+  const int64_t ldy = t.part ? p.N : p.ldy;
+  const bool y_f32 = t.part || t.y_f32;
   if (p.offsets && e == p.n_experts) {   // the rows of dropped slots
-    const int rows = (int)min((int64_t)BM, m1 - m0), cols = (int)min((int64_t)BN, p.N - n0);
-    for (int i = threadIdx.x; i < rows * BN; i += T::NTH)
-      if (i % BN < cols) store1<YF32>(p.y, (m0 + i / BN) * p.ldy + n0 + i % BN, 0.0f);
+    const int rows = (int)min((int64_t)BM, m1 - m0), cols = (int)min((int64_t)TILE_BN, p.N - n0);
+    for (int i = threadIdx.x; i < rows * TILE_BN; i += TILE_NW * 64)
+      if (i % TILE_BN < cols) {
+        const int64_t at = (m0 + i / TILE_BN) * ldy + n0 + i % TILE_BN;
+        y_f32 ? store1<true>(y, at, 0.0f) : store1<false>(y, at, 0.0f);
+      }
     return;
   }
-  const int64_t kb = p.K / 2;
-  // x: lane offsets of the wave's pieces (rows past the group read its last row; not stored)
-  uint32_t xoff[T::PIECES];
+
+  // x: lane offsets of the wave's 8-row pieces (rows past the group read its last row; not stored)
+  uint32_t xoff[TM];
 #pragma unroll
-  for (int j = 0; j < T::PIECES; ++j) {
-    const int r = (wave * T::PIECES + j) * 8 + (lane >> 3);
+  for (int j = 0; j < TM; ++j) {
+    const int r = (wave * TM + j) * 8 + (lane >> 3);
     const int rc = (int)min((int64_t)r, m1 - 1 - m0);
     xoff[j] = (uint32_t)(rc * p.ldx * 2) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
   }
-  const char* xbase = uniform_ptr(p.x + m0 * p.ldx * 2);
-  const int ksteps = (int)(p.K / BK), steps = ksteps * planes;
-  // weight: this thread's half rows
-  const uint8_t* qp[T::TASKS];
-  const uint8_t* sp[T::TASKS];
+  const int ksteps = (int)(p.K / BK);
+  const int k0 = (int)((int64_t)ksteps * slice / t.slices), k1 = (int)((int64_t)ksteps * (slice + 1) / t.slices);
+  const char* xsrc = uniform_ptr(p.x + m0 * p.ldx * 2 + (int64_t)k0 * ROWB);   // the next rows to copy
+  const int steps = (k1 - k0) * PLANES;
+  int xplane = 0;
+  auto copy_x = [&](char* buf) {
 #pragma unroll
-  for (int j = 0; j < T::TASKS; ++j) {
-    const int task = j * T::NTH + threadIdx.x, r = task >> 1, h = task & 1;
-    const int64_t n = min(n0 + r, p.N - 1);
-    qp[j] = p.q + ((int64_t)e * p.N + n) * kb + h * 16;
-    const uint8_t* s = p.s + (int64_t)e * p.s_stride;
-    if constexpr (LAYOUT == 0) sp[j] = s + n * (p.K / B) + h * (32 / B);
-    else if constexpr (LAYOUT == 1) sp[j] = s + (n / 16) * (p.K / 16) + h * 2;
-    else sp[j] = s + (int64_t)(h * 2) * (p.N / 16) + n / 16;
+    for (int j = 0; j < TM; ++j) dma16(xsrc, xoff[j], buf + (wave * TM + j) * 1024);
+    if (PLANES == 1) {
+      xsrc += ROWB;
+    } else {
+      const bool wrap = ++xplane == PLANES;
+      xsrc += wrap ? ROWB - (PLANES - 1) * t.plane_bytes : t.plane_bytes;
+      xplane = wrap ? 0 : xplane;
+    }
+  };
+
+  // weight: this lane's rows
+  const int fr = lane & 31, fk = lane >> 5;
+  constexpr int NS = E8 || B == 32 ? 1 : 2;   // scale codes of 32 codes
+  const uint8_t* qp[TN];
+  const uint8_t* sp[TN];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const int64_t n = min(n0 + wave * OW + i * 32 + fr, p.N - 1);
+    qp[i] = p.q + ((int64_t)e * p.N + n) * (p.K / 2) + (int64_t)k0 * (BK / 2) + fk * 16;
+    sp[i] = p.s + (int64_t)e * p.s_stride + (n >> t.s_band) * t.s_row + ((int64_t)k0 * 2 + fk) * NS * t.s_k;
   }
-  v4u codes[T::TASKS];
-  uint32_t sc[T::TASKS][2];
-  auto load_codes = [&](int step) {
-    const int k = step % ksteps;
+  v4u codes[TN], cnext[TN];
+  uint32_t sc[TN], snext[TN];
+  auto load_codes = [&] {
 #pragma unroll
-    for (int j = 0; j < T::TASKS; ++j) {
-      codes[j] = *reinterpret_cast<const v4u*>(qp[j] + (int64_t)k * (BK / 2));
-      if constexpr (LAYOUT == 2) {
-        sc[j][0] = sp[j][(int64_t)k * 4 * (p.N / 16)];
-        sc[j][1] = sp[j][(int64_t)(k * 4 + 1) * (p.N / 16)];
-      } else if constexpr (B == 16) {
-        const uint32_t c = *reinterpret_cast<const uint16_t*>(sp[j] + k * 4);
-        sc[j][0] = c & 0xFFu;
-        sc[j][1] = c >> 8;
+    for (int i = 0; i < TN; ++i) {
+      cnext[i] = *reinterpret_cast<const v4u*>(qp[i]);
+      qp[i] += BK / 2;
+      if constexpr (NS == 1) {
+        snext[i] = sp[i][0];
+        sp[i] += 2;
+      } else if (t.s_k == 1) {
+        snext[i] = *reinterpret_cast<const uint16_t*>(sp[i]);
+        sp[i] += 4;
       } else {
-        sc[j][0] = sc[j][1] = sp[j][k * 2];
+        snext[i] = sp[i][0] | (uint32_t)sp[i][t.s_k] << 8;
+        sp[i] += 4 * t.s_k;
       }
     }
   };
-  auto write_weight = [&](char* buf) {
+  auto take_codes = [&] {
 #pragma unroll
-    for (int j = 0; j < T::TASKS; ++j) {
-      const int task = j * T::NTH + threadIdx.x, r = task >> 1, h = task & 1;
-      const float s0 = wscale<FMT>(sc[j][0]), s1 = B == 16 ? wscale<FMT>(sc[j][1]) : s0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        *reinterpret_cast<v8bf*>(buf + BM * ROWB + swz(r, h * 4 + c)) = decode8_bf16<FMT>(codes[j][c], c < 2 ? s0 : s1);
+    for (int i = 0; i < TN; ++i) {
+      codes[i] = cnext[i];
+      sc[i] = snext[i];
     }
   };
-  auto copy_x = [&](int step, char* buf) {
-    const char* src = xbase + (int64_t)(step / ksteps) * plane_bytes + (int64_t)(step % ksteps) * ROWB;
-#pragma unroll
-    for (int j = 0; j < T::PIECES; ++j) dma16(src, xoff[j], buf + (wave * T::PIECES + j) * 1024);
+  auto scale = [&](uint32_t c) {
+    // 3 mantissa bits: the code's bits as a float32 times 2^(127 - bias), subnormals included
+    return E8 ? wscale<FMT_E8M0>(c) : __uint_as_float(c << 20) * t.scale_mul;
+  };
+  auto decode = [&](int i, int s) {   // dword s: k = 32 (lane / 32) + 8 s ..
+    const float sv = scale(NS == 1 ? sc[i] : (s < 2 ? sc[i] & 0xFFu : sc[i] >> 8));
+    return decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(codes[i][s], sv);
   };
 
-  v16f acc[T::TN][T::TM];
+  v16f acc[TN][TM];
 #pragma unroll
-  for (int i = 0; i < T::TN; ++i)
+  for (int i = 0; i < TN; ++i)
 #pragma unroll
-    for (int j = 0; j < T::TM; ++j)
+    for (int j = 0; j < TM; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  const int wm = wave % T::WM, wn = wave / T::WM;
-  const int fr = lane & 31, fk = lane >> 5;
 
-  copy_x(0, lds);
-  load_codes(0);
-  write_weight(lds);
-  if (steps > 1) load_codes(1);
+  char* buf = lds;
+  char* nxt = lds + STAGE;
+  copy_x(buf);
+  if (steps > 1) copy_x(nxt);
+  load_codes();
+  take_codes();
+  if (k0 + 1 < k1) load_codes();
+  v8bf bw[TN][4];
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) bw[i][s] = decode(i, s);
   wait_copies();
   __syncthreads();
+  v8bf ax[2][TM];
+  auto read_x = [&](const char* from, int s, v8bf* to) {
+#pragma unroll
+    for (int j = 0; j < TM; ++j) to[j] = *reinterpret_cast<const v8bf*>(from + swz(j * 32 + fr, fk * 4 + s));
+  };
+  read_x(buf, 0, ax[0]);
+  int plane = 0, k = k0;
   for (int st = 0; st < steps; ++st) {
-    char* buf = lds + (st & 1) * T::STAGE;
-    char* nxt = lds + ((st & 1) ^ 1) * T::STAGE;
-    if (st + 1 < steps) {
-      copy_x(st + 1, nxt);
-      write_weight(nxt);
-      if (st + 2 < steps) load_codes(st + 2);
+    // the last part of x at this k: the codes of k + 1 replace those of k behind their last use
+    const bool turn = PLANES == 1 || plane == PLANES - 1, more = k + 1 < k1;
+    if (turn && more) {
+      take_codes();
+      if (k + 2 < k1) load_codes();
     }
 #pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      v8bf a[T::TN], b[T::TM];
+    for (int s = 0; s < 4; ++s) {
+      if (s == 3) {
+        if (st + 1 < steps) {
+          wait_copies();
+          __syncthreads();
+          if (st + 2 < steps) copy_x(buf);
+          read_x(nxt, 0, ax[0]);
+        }
+      } else {
+        read_x(buf, s + 1, ax[(s + 1) & 1]);
+      }
 #pragma unroll
-      for (int i = 0; i < T::TN; ++i)
-        a[i] = *reinterpret_cast<const v8bf*>(buf + BM * ROWB + swz((wn * T::TN + i) * 32 + fr, kk * 2 + fk));
+      for (int j = 0; j < TM; ++j)
 #pragma unroll
-      for (int j = 0; j < T::TM; ++j)
-        b[j] = *reinterpret_cast<const v8bf*>(buf + swz((wm * T::TM + j) * 32 + fr, kk * 2 + fk));
+        for (int i = 0; i < TN; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[i][s], ax[s & 1][j], acc[i][j], 0, 0, 0);
+      if (turn && more) {
 #pragma unroll
-      for (int i = 0; i < T::TN; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < TN; ++i) bw[i][s] = decode(i, s);
+      }
     }
-    wait_copies();
-    __syncthreads();
+    if (PLANES > 1) plane = turn ? 0 : plane + 1;
+    if (turn) ++k;
+    char* const b = buf;
+    buf = nxt;
+    nxt = b;
   }
+  __syncthreads();
 
   // Out: lane l of a product holds row m = l % 32 and columns n = 8 (r / 4) + 4 (l / 32) + r % 4.
-  // Each wave turns 32 rows of its columns at a time through its own LDS rows (padded by 16 bytes).
-  constexpr int OW = T::TN * 32, OLD = OW + 4;
+  // Each wave turns 32 rows of its columns at a time through its own LDS rows.
   float* out = reinterpret_cast<float*>(lds) + wave * 32 * OLD;
-  static_assert(T::NW * 32 * OLD * 4 <= 2 * T::STAGE, "the output rows fit the buffers");
-  const int64_t c0 = n0 + wn * OW;
+  const int64_t c0 = n0 + wave * OW;
   const float* g = p.g ? p.g + (int64_t)e * p.g_stride : nullptr;
 #pragma unroll
-  for (int j = 0; j < T::TM; ++j) {
+  for (int j = 0; j < TM; ++j) {
 #pragma unroll
-    for (int i = 0; i < T::TN; ++i)
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
         v4f v;
@@ -431,20 +489,37 @@ __global__ __launch_bounds__(T::NTH) void k_wlinear_tile(WParams p, int planes, 
         *reinterpret_cast<v4f*>(out + fr * OLD + i * 32 + r4 * 8 + fk * 4) = v;
       }
     wave_lds_order();
-    const int64_t mrow = m0 + (wm * T::TM + j) * 32;
 #pragma unroll 4
     for (int o = lane; o < 32 * OW / 4; o += 64) {
       const int r = o / (OW / 4), c = (o % (OW / 4)) * 4;
       const v4f v = *reinterpret_cast<const v4f*>(out + r * OLD + c);
-      const int64_t m = mrow + r, n = c0 + c;
-      if (m < m1) {
+      const int64_t m = m0 + j * 32 + r, n = c0 + c;
+      if (m >= m1 || n >= p.N) continue;
+      const float gn = g ? g[p.g_shift ? n >> p.g_shift : 0] : 1.0f;   // stripes are multiples of 16 columns
+      const int64_t at = m * ldy + n;
+      if (t.y_vec && n + 4 <= p.N) {
+        if (y_f32) *reinterpret_cast<v4f*>(y + at * 4) = v4f{v[0] * gn, v[1] * gn, v[2] * gn, v[3] * gn};
+        else *reinterpret_cast<uint64_t*>(y + at * 2) =
+                 (uint64_t)pack_bf16(v[2] * gn, v[3] * gn) << 32 | pack_bf16(v[0] * gn, v[1] * gn);
+      } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (n + k < p.N)
-            store1<YF32>(p.y, m * p.ldy + n + k, v[k] * (g ? g[p.g_shift ? (n + k) >> p.g_shift : 0] : 1.0f));
+        for (int q = 0; q < 4; ++q)
+          if (n + q < p.N) y_f32 ? store1<true>(y, at + q, v[q] * gn) : store1<false>(y, at + q, v[q] * gn);
       }
     }
     wave_lds_order();
+  }
+}
+
+// The slices' sums in slice order, rounded once to y's type.
+template <bool YF32>
+__global__ __launch_bounds__(256) void k_join_slices(const float* __restrict__ part, int slices, int64_t rows, int64_t N,
+                                                     char* __restrict__ y, int64_t ldy) {
+  const int64_t n = rows * N;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float v = part[i];
+    for (int s = 1; s < slices; ++s) v += part[s * n + i];
+    store1<YF32>(y, i / N * ldy + i % N, v);
   }
 }
 
@@ -472,63 +547,104 @@ __global__ __launch_bounds__(256) void k_zero_rows(char* y, int64_t rows, int64_
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-using Tile256 = WTile<2, 4, 4, 2>;
-using Tile128 = WTile<2, 2, 2, 2>;
-
 // Rows per expert (on average) from which the tile form is used.
-bool use_tile(const WLinearArgs& a) { return a.rows / a.n_experts > 64 && a.ldx <= (int64_t(1) << 22); }
+bool use_tile(const WLinearArgs& a) { return a.rows / a.n_experts > 16 && a.ldx <= (int64_t(1) << 22); }
 
-template <int FMT, int B, int LAYOUT, bool YF32, class T>
-hipError_t launch_tile(const WLinearArgs& a, WParams p) {
-  int planes = 1;
+struct TilePlan {
+  int tm;          // 32-row products per tile
+  int64_t mt, nt;  // tiles, at most
+  int slices;      // parts of K
+};
+
+TilePlan plan_tiles(const WLinearArgs& a) {
+  TilePlan t;
+  const int64_t avg = a.rows / a.n_experts;
+  t.nt = div_up(a.N, TILE_BN);
+  t.tm = avg <= 32 ? 1 : avg <= 64 ? 2 : 4;
+  if (div_up(a.rows, 256) * t.nt >= 256) t.tm = 8;
+  t.mt = div_up(a.rows, t.tm * 32) + (a.offsets ? a.n_experts : 0);
+  const int64_t tiles = div_up(a.rows, t.tm * 32) * t.nt;
+  t.slices = (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, a.K / BK / 4));
+  return t;
+}
+
+size_t planes_bytes(const WLinearArgs& a) { return a.x_f32 ? (size_t)div_up(3 * a.rows * a.K * 2, 256) * 256 : 0; }
+
+template <bool E8, int B, int PLANES>
+void launch_tile(const WLinearArgs& a, const WParams& p, const TileArgs& t, int tm) {
+  const uint32_t grid = (uint32_t)(div_up((int64_t)t.mtiles * t.ntiles * t.slices, 8) * 8);
+  if (tm == 1) k_wlinear_tile<E8, B, PLANES, 1><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
+  else if (tm == 2) k_wlinear_tile<E8, B, PLANES, 2><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
+  else if (tm == 4) k_wlinear_tile<E8, B, PLANES, 4><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
+  else k_wlinear_tile<E8, B, PLANES, 8><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
+}
+
+void run_tiles(const WLinearArgs& a, WParams p) {
+  const TilePlan plan = plan_tiles(a);
   if (a.x_f32) {
     const uint32_t grid = (uint32_t)std::min<int64_t>(div_up(a.rows * (a.K / 8), 256), 8192);
     k_split3<<<grid, 256, 0, a.stream>>>((const float*)a.x, a.ldx, a.rows, a.K, (char*)a.ws);
-    planes = 3;
     p.x = (const char*)a.ws;
     p.ldx = a.K;
   }
-  const int64_t mt = div_up(a.rows, T::BM) + (a.offsets ? a.n_experts : 0), nt = div_up(a.N, T::BN);
-  const int64_t grid = div_up(mt * nt, 8) * 8;
-  k_wlinear_tile<FMT, B, LAYOUT, YF32, T><<<(uint32_t)grid, T::NTH, 0, a.stream>>>(
-      p, planes, a.rows * a.K * 2, (uint32_t)mt, (uint32_t)nt);
-  return hipSuccess;
+  TileArgs t{};
+  t.mtiles = (uint32_t)plan.mt;
+  t.ntiles = (uint32_t)plan.nt;
+  t.slices = plan.slices;
+  t.plane_bytes = a.rows * a.K * 2;
+  t.y_f32 = a.y_f32;
+  if (plan.slices > 1) t.part = reinterpret_cast<float*>((char*)a.ws + planes_bytes(a));
+  const int64_t esz = t.part || a.y_f32 ? 4 : 2, ld = t.part ? a.N : a.ldy;
+  t.y_vec = (ld * esz) % (4 * esz) == 0 && (t.part || reinterpret_cast<uintptr_t>(a.y) % (4 * esz) == 0);
+  t.scale_mul = a.fmt == FMT_E4M3 ? 0x1p120f : 0x1p112f;
+  t.s_band = a.layout == 0 ? 0 : 4;
+  t.s_row = a.layout == 0 ? a.K / a.block : a.layout == 1 ? a.K / 16 : 1;
+  t.s_k = a.layout == 2 ? a.N / 16 : 1;
+  if (a.fmt == FMT_E8M0) a.x_f32 ? launch_tile<true, 32, 3>(a, p, t, plan.tm) : launch_tile<true, 32, 1>(a, p, t, plan.tm);
+  else if (a.block == 16) a.x_f32 ? launch_tile<false, 16, 3>(a, p, t, plan.tm) : launch_tile<false, 16, 1>(a, p, t, plan.tm);
+  else a.x_f32 ? launch_tile<false, 32, 3>(a, p, t, plan.tm) : launch_tile<false, 32, 1>(a, p, t, plan.tm);
+  if (t.part) {
+    const uint32_t grid = (uint32_t)std::min<int64_t>(div_up(a.rows * a.N, 256), 4096);
+    if (a.y_f32) k_join_slices<true><<<grid, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
+    else k_join_slices<false><<<grid, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
+  }
 }
 
 template <int FMT, int B, int LAYOUT, bool XF32, bool YF32>
-hipError_t launch(const WLinearArgs& a, const WParams& p) {
-  if (use_tile(a)) {
-    const int64_t big = div_up(a.rows, 256) * div_up(a.N, 256);
-    if (big >= 256) return launch_tile<FMT, B, LAYOUT, YF32, Tile256>(a, p);
-    return launch_tile<FMT, B, LAYOUT, YF32, Tile128>(a, p);
-  }
+void launch(const WLinearArgs& a, const WParams& p) {
   const dim3 grid((uint32_t)div_up(a.N, 16), (uint32_t)(a.offsets ? a.n_experts + 1 : 1));
   const int64_t avg = a.rows / a.n_experts;
   if (avg <= 16) k_wlinear_rows<FMT, B, LAYOUT, XF32, YF32, 1, 8><<<grid, 512, 0, a.stream>>>(p);
   else k_wlinear_rows<FMT, B, LAYOUT, XF32, YF32, 4, 4><<<grid, 256, 0, a.stream>>>(p);
-  return hipSuccess;
 }
 
 template <int FMT, int B, int LAYOUT>
-hipError_t by_types(const WLinearArgs& a, const WParams& p) {
-  if (a.x_f32) return a.y_f32 ? launch<FMT, B, LAYOUT, true, true>(a, p) : launch<FMT, B, LAYOUT, true, false>(a, p);
-  return a.y_f32 ? launch<FMT, B, LAYOUT, false, true>(a, p) : launch<FMT, B, LAYOUT, false, false>(a, p);
+void by_types(const WLinearArgs& a, const WParams& p) {
+  if (a.x_f32) a.y_f32 ? launch<FMT, B, LAYOUT, true, true>(a, p) : launch<FMT, B, LAYOUT, true, false>(a, p);
+  else a.y_f32 ? launch<FMT, B, LAYOUT, false, true>(a, p) : launch<FMT, B, LAYOUT, false, false>(a, p);
 }
 
 template <int FMT>
-hipError_t by_layout(const WLinearArgs& a, const WParams& p) {
+void by_layout(const WLinearArgs& a, const WParams& p) {
   if constexpr (FMT != FMT_E8M0) {
-    if (a.block == 16 && a.layout == 0) return by_types<FMT, 16, 0>(a, p);
-    if (a.block == 16 && a.layout == 1) return by_types<FMT, 16, 1>(a, p);
-    if (a.block == 16) return by_types<FMT, 16, 2>(a, p);
+    if (a.block == 16) {
+      if (a.layout == 0) by_types<FMT, 16, 0>(a, p);
+      else if (a.layout == 1) by_types<FMT, 16, 1>(a, p);
+      else by_types<FMT, 16, 2>(a, p);
+      return;
+    }
   }
-  return by_types<FMT, 32, 0>(a, p);
+  by_types<FMT, 32, 0>(a, p);
 }
 
 }  // namespace
 
-// the three bf16 planes of float32 activations in the tile form
-size_t wlinear_ws(const WLinearArgs& a) { return a.x_f32 && use_tile(a) ? (size_t)(3 * a.rows * a.K * 2) : 0; }
+// the tile form's bf16 parts of float32 activations and the sums of a split K
+size_t wlinear_ws(const WLinearArgs& a) {
+  if (!use_tile(a) || a.rows == 0 || a.N == 0 || a.K == 0) return 0;
+  const TilePlan t = plan_tiles(a);
+  return planes_bytes(a) + (t.slices > 1 ? (size_t)t.slices * a.rows * a.N * 4 : 0);
+}
 
 hipError_t run_wlinear(const WLinearArgs& a) {
   if (a.rows == 0 || a.N == 0) return hipSuccess;
@@ -554,10 +670,11 @@ hipError_t run_wlinear(const WLinearArgs& a) {
   p.ldy = a.ldy;
   p.s_stride = a.layout == 0 ? a.N * (a.K / a.block) : (a.N / 16) * (a.K / 16);
   p.g_stride = a.g_shift ? div_up(a.N, int64_t(1) << a.g_shift) : 1;
-  const hipError_t err = a.fmt == FMT_E8M0   ? by_layout<FMT_E8M0>(a, p)
-                         : a.fmt == FMT_E4M3 ? by_layout<FMT_E4M3>(a, p)
-                                             : by_layout<FMT_UE5M3>(a, p);
-  return err != hipSuccess ? err : hipGetLastError();
+  if (use_tile(a)) run_tiles(a, p);
+  else if (a.fmt == FMT_E8M0) by_layout<FMT_E8M0>(a, p);
+  else if (a.fmt == FMT_E4M3) by_layout<FMT_E4M3>(a, p);
+  else by_layout<FMT_UE5M3>(a, p);
+  return hipGetLastError();
 }
 
 }  // namespace fp4k
