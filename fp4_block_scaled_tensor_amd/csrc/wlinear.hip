@@ -35,6 +35,8 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
 }
+template <class T>
+__device__ __forceinline__ void pin(T& v) { asm volatile("" : "+v"(v)); }
 // this wave's copies have landed and its LDS reads are done
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
@@ -372,29 +374,36 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(
     sp[i] = p.s + (int64_t)e * p.s_stride + (n >> t.s_band) * t.s_row + ((int64_t)k0 * 2 + fk) * NS * t.s_k;
   }
   v4u codes[TN], cnext[TN];
-  uint32_t sc[TN], snext[TN];
-  auto load_codes = [&] {
+  uint32_t sc[TN][NS], snext[TN][NS];
+  int kload = k0;
+  auto load_codes = [&] {   // the step kload; past the slice's last step that step again (not used), without a branch
+    const int64_t on = kload + 1 < k1 ? 1 : 0;
+    ++kload;
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       cnext[i] = *reinterpret_cast<const v4u*>(qp[i]);
-      qp[i] += BK / 2;
-      if constexpr (NS == 1) {
-        snext[i] = sp[i][0];
-        sp[i] += 2;
-      } else if (t.s_k == 1) {
-        snext[i] = *reinterpret_cast<const uint16_t*>(sp[i]);
-        sp[i] += 4;
-      } else {
-        snext[i] = sp[i][0] | (uint32_t)sp[i][t.s_k] << 8;
-        sp[i] += 4 * t.s_k;
-      }
+      qp[i] += on * (BK / 2);
+#pragma unroll
+      for (int h = 0; h < NS; ++h) snext[i][h] = sp[i][h * t.s_k];
+      sp[i] += on * 2 * NS * t.s_k;
+    }
+  };
+  // The codes have landed (after wait_copies()): without this the compiler, which does not see that
+  // wait, waits at their first use for every copy issued since.
+  auto pin_codes = [&] {
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      pin(cnext[i]);
+#pragma unroll
+      for (int h = 0; h < NS; ++h) pin(snext[i][h]);
     }
   };
   auto take_codes = [&] {
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       codes[i] = cnext[i];
-      sc[i] = snext[i];
+#pragma unroll
+      for (int h = 0; h < NS; ++h) sc[i][h] = snext[i][h];
     }
   };
   auto scale = [&](uint32_t c) {
@@ -402,7 +411,7 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(
     return E8 ? wscale<FMT_E8M0>(c) : __uint_as_float(c << 20) * t.scale_mul;
   };
   auto decode = [&](int i, int s) {   // dword s: k = 32 (lane / 32) + 8 s ..
-    const float sv = scale(NS == 1 ? sc[i] : (s < 2 ? sc[i] & 0xFFu : sc[i] >> 8));
+    const float sv = scale(sc[i][s * NS / 4]);
     return decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(codes[i][s], sv);
   };
 
@@ -420,13 +429,14 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(
   if (steps > 1) copy_x(nxt);
   load_codes();
   take_codes();
-  if (k0 + 1 < k1) load_codes();
-  v8bf bw[TN][4];
+  load_codes();
+  v8bf bw[TN][4];   // the decoded weight of a step, dword by dword
 #pragma unroll
-  for (int i = 0; i < TN; ++i)
+  for (int s = 0; s < 3; ++s)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) bw[i][s] = decode(i, s);
+    for (int i = 0; i < TN; ++i) bw[i][s] = decode(i, s);
   wait_copies();
+  pin_codes();
   __syncthreads();
   v8bf ax[2][TM];
   auto read_x = [&](const char* from, int s, v8bf* to) {
@@ -434,23 +444,19 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(
     for (int j = 0; j < TM; ++j) to[j] = *reinterpret_cast<const v8bf*>(from + swz(j * 32 + fr, fk * 4 + s));
   };
   read_x(buf, 0, ax[0]);
-  int plane = 0, k = k0;
+  int plane = 0;
   for (int st = 0; st < steps; ++st) {
-    // the last part of x at this k: the codes of k + 1 replace those of k behind their last use
-    const bool turn = PLANES == 1 || plane == PLANES - 1, more = k + 1 < k1;
-    if (turn && more) {
-      take_codes();
-      if (k + 2 < k1) load_codes();
-    }
+    const bool first = PLANES == 1 || plane == 0, last = PLANES == 1 || plane == PLANES - 1;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s == 3) {
-        if (st + 1 < steps) {
-          wait_copies();
-          __syncthreads();
-          if (st + 2 < steps) copy_x(buf);
-          read_x(nxt, 0, ax[0]);
-        }
+        // (past the last step: an unused read of the other buffer, so that no path joins here with
+        // this step's fragments still being waited for)
+        wait_copies();
+        pin_codes();
+        __syncthreads();
+        if (st + 2 < steps) copy_x(buf);
+        read_x(nxt, 0, ax[0]);
       } else {
         read_x(buf, s + 1, ax[(s + 1) & 1]);
       }
@@ -459,18 +465,30 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(
 #pragma unroll
         for (int i = 0; i < TN; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[i][s], ax[s & 1][j], acc[i][j], 0, 0, 0);
-      if (turn && more) {
+      // group 0 decodes this step's last dword; groups 1 to 3 replace dwords 0 to 2, whose products
+      // are under way, by the next step's
+      if (s == 0 ? first : last) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i) bw[i][s] = decode(i, s);
+        for (int i = 0; i < TN; ++i) bw[i][(s + 3) & 3] = decode(i, (s + 3) & 3);
       }
+      if (s == 0 && last) {
+        take_codes();
+        load_codes();
+      }
+      // per TN products one fragment read and a share of the decoding
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, TN, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, ((E8 ? 6 : 19) * TN + TM - 1) / TM, 0);
+      }
+      if (s == 0) __builtin_amdgcn_sched_group_barrier(0x020, TN * (1 + NS), 0);   // the next step's codes
     }
-    if (PLANES > 1) plane = turn ? 0 : plane + 1;
-    if (turn) ++k;
+    if (PLANES > 1) plane = last ? 0 : plane + 1;
     char* const b = buf;
     buf = nxt;
     nxt = b;
   }
-  __syncthreads();
 
   // Out: lane l of a product holds row m = l % 32 and columns n = 8 (r / 4) + 4 (l / 32) + r % 4.
   // Each wave turns 32 rows of its columns at a time through its own LDS rows.
