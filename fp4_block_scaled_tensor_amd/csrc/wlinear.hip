@@ -252,49 +252,59 @@ __global__ __launch_bounds__(NW * 64) void k_wlinear_rows(WParams p) {
 // An LDS row is 128 bytes (64 k); 16-byte chunk j of row r sits at position j ^ ((r >> 1) & 7), so
 // sixteen consecutive rows reading one logical chunk cover all banks.
 constexpr int BK = 64, ROWB = BK * 2;
-constexpr int TILE_NW = 4, TILE_TN = 2, TILE_BN = TILE_NW * TILE_TN * 32;
+constexpr int TILE_BN = 256;   // columns (weight rows) of a tile
 
 __device__ __forceinline__ uint32_t swz(int row, int chunk) { return row * ROWB + ((chunk ^ ((row >> 1) & 7)) << 4); }
 
-// The m-tile `mt` of the grouped rows: its expert and first row; false past the last one. The
-// experts' tiles follow each other; the rows of dropped slots are the last group.
+// The m-tiles of the grouped rows: the experts' tiles follow each other, the rows of dropped slots
+// are the last group. Lane l holds group l of the current 64 (all of them for up to 63 experts).
 template <int BM>
-__device__ __forceinline__ bool find_tile(const WParams& p, int64_t mt, int& e, int64_t& m0, int64_t& m1) {
-  if (!p.offsets) {
-    e = 0;
-    m0 = mt * BM;
-    m1 = p.rows;
-    return m0 < m1;
-  }
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int e0 = 0; e0 <= p.n_experts; e0 += 64) {
-    int64_t lo = 0, hi = 0;
-    if (e0 + lane <= p.n_experts) group_rows(p, e0 + lane, lo, hi);
-    const int t = (int)((max(hi - lo, (int64_t)0) + BM - 1) / BM);
-    int s = t;
+struct TileMap {
+  int lo, hi, tiles, upto;   // rows, tiles, tiles of this and the groups before it (in the 64)
+  __device__ __forceinline__ void load(const WParams& p, int g0) {
+    const int lane = threadIdx.x & 63;
+    int64_t a = 0, b = 0;
+    if (g0 + lane <= p.n_experts) group_rows(p, g0 + lane, a, b);
+    lo = (int)a;   // rows fit 31 bits
+    hi = (int)b;
+    tiles = (max(hi - lo, 0) + BM - 1) / BM;
+    upto = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(s, o, 64);
-      if (lane >= o) s += u;
+      const int u = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += u;
     }
-    const uint64_t past = __ballot(before + s > mt);
-    if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      // wave-uniform (rows fit 31 bits)
-      e = __builtin_amdgcn_readfirstlane(e0 + l);
-      const int first = before + __shfl(s - t, l, 64);
-      m1 = __builtin_amdgcn_readfirstlane(__shfl((int)hi, l, 64));
-      m0 = __builtin_amdgcn_readfirstlane(__shfl((int)lo, l, 64) + ((int)mt - first) * BM);
-      return true;
-    }
-    before += __shfl(s, 63, 64);
   }
-  return false;
-}
+  // all tiles; leaves the first 64 groups loaded
+  __device__ __forceinline__ uint32_t count(const WParams& p) {
+    int n = 0;
+    for (int g0 = (p.n_experts / 64) * 64; g0 >= 0; g0 -= 64) {
+      load(p, g0);
+      n += __shfl(upto, 63, 64);
+    }
+    return __builtin_amdgcn_readfirstlane(n);
+  }
+  // after count(): tile mt's group, first row and the group's end, wave-uniform; mt is below the count
+  __device__ __forceinline__ void find(const WParams& p, int mt, int& e, int64_t& m0, int64_t& m1) {
+    int before = 0;
+    for (int g0 = 0;;) {
+      const uint64_t past = __ballot(before + upto > mt);
+      if (past) {
+        const int l = __ffsll((unsigned long long)past) - 1;
+        e = __builtin_amdgcn_readfirstlane(g0 + l);
+        m1 = __builtin_amdgcn_readfirstlane(__shfl(hi, l, 64));
+        m0 = __builtin_amdgcn_readfirstlane(__shfl(lo, l, 64) + (mt - before - __shfl(upto - tiles, l, 64)) * BM);
+        return;
+      }
+      before += __shfl(upto, 63, 64);
+      g0 += 64;
+      load(p, g0);
+    }
+  }
+};
 
 struct TileArgs {
-  uint32_t mtiles, ntiles;
+  uint32_t mtiles, ntiles;   // mtiles: an upper bound with offsets
   int slices;            // parts of K, each with its own output rows in `part`
   int64_t plane_bytes;   // bytes between the bf16 parts of float32 activations
   bool y_f32, y_vec;     // y_vec: rows of y take 4-element stores
@@ -305,25 +315,29 @@ struct TileArgs {
 };
 
 // E8: power-of-two scales (block 32), else 3-mantissa-bit ones with block B. PLANES: bf16 parts of x.
-template <bool E8, int B, int PLANES, int TM>
-__global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(WParams p, TileArgs t) {
-  constexpr int BM = TM * 32, STAGE = BM * ROWB, TN = TILE_TN;
+template <bool E8, int B, int PLANES, int TM, int TILE_NW>
+__global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void k_wlinear_tile(WParams p, TileArgs t) {
+  constexpr int BM = TM * 32, STAGE = BM * ROWB, TN = TILE_BN / 32 / TILE_NW, PIECES = BM / 8 / TILE_NW;
   constexpr int OW = TN * 32, OLD = OW + 4;   // a wave's output columns, padded by 16 bytes
   constexpr int OUTB = TILE_NW * 32 * OLD * 4;
   __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE > OUTB ? 2 * STAGE : OUTB];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // workgroup ids go round-robin over the 8 dies: give each die a contiguous run of tiles, in
-  // groups of 4 m-tiles that share the weight tile in its L2
-  const uint32_t tiles = t.mtiles * t.ntiles, total = tiles * t.slices, per = (total + 7) / 8;
-  const uint32_t all = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (all >= total) return;
+  TileMap<BM> map;
+  const uint32_t mtiles = p.offsets ? map.count(p) : t.mtiles;
+  // workgroup ids go round-robin over the 8 dies: give each die a contiguous run of the tiles that
+  // there are (not of those that there might be: the dies would be loaded unevenly), in groups of 4
+  // m-tiles that share the weight tile in its L2
+  const uint32_t tiles = mtiles * t.ntiles, total = tiles * t.slices, per = (total + 7) / 8;
+  const uint32_t in_die = blockIdx.x >> 3, all = (blockIdx.x & 7) * per + in_die;
+  if (in_die >= per || all >= total) return;
   const uint32_t slice = all / tiles, id = all - slice * tiles;
   constexpr uint32_t GM = 4;
-  const uint32_t grp = id / (GM * t.ntiles), gm = min(GM, t.mtiles - grp * GM), rest = id - grp * GM * t.ntiles;
-  const int64_t mt = grp * GM + rest % gm, n0 = (int64_t)(rest / gm) * TILE_BN;
-  int e;
-  int64_t m0, m1;
-  if (!find_tile<BM>(p, mt, e, m0, m1)) return;
+  const uint32_t grp = id / (GM * t.ntiles), gm = min(GM, mtiles - grp * GM), rest = id - grp * GM * t.ntiles;
+  const int mt = grp * GM + rest % gm;
+  const int64_t n0 = (int64_t)(rest / gm) * TILE_BN;
+  int e = 0;
+  int64_t m0 = (int64_t)mt * BM, m1 = p.rows;
+  if (p.offsets) map.find(p, mt, e, m0, m1);
   char* y = t.part ? reinterpret_cast<char*>(t.part + (int64_t)slice * p.rows * p.N) : p.y;
   const int64_t ldy = t.part ? p.N : p.ldy;
   const bool y_f32 = t.part || t.y_f32;
@@ -338,10 +352,10 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(
   }
 
   // x: lane offsets of the wave's 8-row pieces (rows past the group read its last row; not stored)
-  uint32_t xoff[TM];
+  uint32_t xoff[PIECES];
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int r = (wave * TM + j) * 8 + (lane >> 3);
+  for (int j = 0; j < PIECES; ++j) {
+    const int r = (wave * PIECES + j) * 8 + (lane >> 3);
     const int rc = (int)min((int64_t)r, m1 - 1 - m0);
     xoff[j] = (uint32_t)(rc * p.ldx * 2) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
   }
@@ -352,7 +366,7 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 ? 1 : 2) void k_wlinear_tile(
   int xplane = 0;
   auto copy_x = [&](char* buf) {
 #pragma unroll
-    for (int j = 0; j < TM; ++j) dma16(xsrc, xoff[j], buf + (wave * TM + j) * 1024);
+    for (int j = 0; j < PIECES; ++j) dma16(xsrc, xoff[j], buf + (wave * PIECES + j) * 1024);
     if (PLANES == 1) {
       xsrc += ROWB;
     } else {
@@ -591,10 +605,10 @@ size_t planes_bytes(const WLinearArgs& a) { return a.x_f32 ? (size_t)div_up(3 * 
 template <bool E8, int B, int PLANES>
 void launch_tile(const WLinearArgs& a, const WParams& p, const TileArgs& t, int tm) {
   const uint32_t grid = (uint32_t)(div_up((int64_t)t.mtiles * t.ntiles * t.slices, 8) * 8);
-  if (tm == 1) k_wlinear_tile<E8, B, PLANES, 1><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
-  else if (tm == 2) k_wlinear_tile<E8, B, PLANES, 2><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
-  else if (tm == 4) k_wlinear_tile<E8, B, PLANES, 4><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
-  else k_wlinear_tile<E8, B, PLANES, 8><<<grid, TILE_NW * 64, 0, a.stream>>>(p, t);
+  if (tm == 1) k_wlinear_tile<E8, B, PLANES, 1, 4><<<grid, 256, 0, a.stream>>>(p, t);
+  else if (tm == 2) k_wlinear_tile<E8, B, PLANES, 2, 4><<<grid, 256, 0, a.stream>>>(p, t);
+  else if (tm == 4) k_wlinear_tile<E8, B, PLANES, 4, 4><<<grid, 256, 0, a.stream>>>(p, t);
+  else k_wlinear_tile<E8, B, PLANES, 8, 8><<<grid, 512, 0, a.stream>>>(p, t);
 }
 
 void run_tiles(const WLinearArgs& a, WParams p) {
