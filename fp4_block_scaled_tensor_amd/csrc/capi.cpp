@@ -264,6 +264,7 @@ fp4_status check_wlinear(const fp4_operand* w, int64_t rows, int32_t x_dtype, in
   a.N = w->rows;
   a.K = w->k;
   a.n_experts = n_experts ? n_experts : 1;
+  a.offsets_given = n_experts != 0;
   return FP4_OK;
 }
 

@@ -68,6 +68,7 @@ struct WLinearArgs {
   int fmt, block, layout, g_shift;
   int64_t N, K;
   int n_experts;      // 1 without offsets
+  bool offsets_given; // rows in expert order (known before the offsets are)
   const int32_t* offsets;
   void* y;
   void* ws;

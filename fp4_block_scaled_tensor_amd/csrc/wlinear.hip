@@ -129,102 +129,137 @@ __device__ __forceinline__ void store1(char* y, int64_t i, float v) {
   else reinterpret_cast<uint16_t*>(y)[i] = (uint16_t)pack_bf16(v, 0.0f);
 }
 
-// Rows form: a workgroup owns 16 weight rows (one expert's, blockIdx.y) and all of the group's
-// activation rows, 16 TM at a time; its waves split K and join their sums through LDS. Lane l of a
-// 16x16x32 product holds weight row l % 16 and eight consecutive k of K group l / 16; the lane's
-// codes come as 32 consecutive bytes (64 k), so one wave reads 128 consecutive bytes of 16 rows.
-template <int FMT, int B, int LAYOUT, bool XF32, bool YF32, int TM, int NW>
-__global__ __launch_bounds__(NW * 64) void k_wlinear_rows(WParams p) {
-  __shared__ float red[NW][TM * 4][64];
-  const int e = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// What both forms need beside the operands.
+struct FormArgs {
+  int64_t plane_bytes;   // bytes between the bf16 parts of float32 activations
+  bool y_f32, y_vec;     // y_vec: rows of y take 4-element stores
+  float scale_mul;       // 2^(127 - bias) of the 3-mantissa-bit scales
+  int64_t s_row, s_k;    // scale codes: bytes between rows (16-row bands for 2D) and between blocks of K
+  int s_band;            // log2 of the rows that share a scale row (0 or 4)
+};
+
+// E8: power-of-two scales; else 3 mantissa bits: the code's bits as a float32 times 2^(127 - bias),
+// subnormals included
+template <bool E8>
+__device__ __forceinline__ float code_value(uint32_t c, float scale_mul) {
+  return E8 ? wscale<FMT_E8M0>(c) : __uint_as_float(c << 20) * scale_mul;
+}
+
+// ---------------------------------------------------------------- rows form
+// For few activation rows the weight's bytes are the bound. A workgroup owns 16 TN weight rows (one
+// expert's, blockIdx.y) and the group's activation rows, 16 at a time; its eight waves take 256 k
+// each in turn, so that together they read 1 KiB of a row, and join their sums through LDS. Lane l
+// of a 16x16x32 product holds weight row l % 16 and eight consecutive k; its 64 codes of a turn are
+// 32 consecutive bytes of that row, and the next turn's are loaded before this one's are used.
+// Activation rows past the group read its last row: their products are not stored.
+constexpr int ROWS_NW = 8, ROWS_K = 256;
+
+template <bool E8, int B, int PLANES, int TN>
+__global__ __launch_bounds__(ROWS_NW * 64, PLANES == 1 ? 4 : 2) void k_wlinear_rows(WParams p, FormArgs t) {
+  __shared__ float red[ROWS_NW][TN * 4][64];
+  const int e = blockIdx.y, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kg = lane >> 4;
   int64_t lo, hi;
   group_rows(p, e, lo, hi);
   if (lo >= hi) return;
-  const int64_t n0 = (int64_t)blockIdx.x * 16, n = n0 + r;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * TN);
   if (p.offsets && e == p.n_experts) {   // the rows of dropped slots
-    for (int64_t i = threadIdx.x; i < (hi - lo) * 16; i += NW * 64)
-      if (n0 + (i & 15) < p.N) store1<YF32>(p.y, (lo + (i >> 4)) * p.ldy + n0 + (i & 15), 0.0f);
+    for (int64_t i = threadIdx.x; i < (hi - lo) * (16 * TN); i += ROWS_NW * 64) {
+      const int64_t m = lo + i / (16 * TN), n = n0 + i % (16 * TN);
+      if (n < p.N) t.y_f32 ? store1<true>(p.y, m * p.ldy + n, 0.0f) : store1<false>(p.y, m * p.ldy + n, 0.0f);
+    }
     return;
   }
-  const int64_t nr = n < p.N ? n : p.N - 1;   // rows past the weight read the last row and are not stored
-  const uint8_t* q = p.q + (int64_t)e * p.N * (p.K / 2) + nr * (p.K / 2);
-  const uint8_t* s = p.s + (int64_t)e * p.s_stride;
-  for (int64_t m0 = lo; m0 < hi; m0 += 16 * TM) {
-    v4f acc[TM];
+  constexpr int NS = 64 / B;   // scale codes of a lane's 64 codes
+  const uint8_t* q[TN];
+  const uint8_t* sp[TN];
 #pragma unroll
-    for (int t = 0; t < TM; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t kb = (int64_t)wave * 256; kb < p.K; kb += NW * 256) {
-      const int64_t k0 = kb + kg * 64;
-      v4u w[2] = {v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}};
-      float sv[64 / B];
+  for (int i = 0; i < TN; ++i) {
+    const int64_t n = min(n0 + i * 16 + r, p.N - 1);   // rows past the weight read the last one and are not stored
+    q[i] = p.q + ((int64_t)e * p.N + n) * (p.K / 2) + kg * 32;
+    sp[i] = p.s + (int64_t)e * p.s_stride + (n >> t.s_band) * t.s_row + kg * NS * t.s_k;
+  }
+  struct Codes {
+    v4u w[2];
+    uint32_t s;
+  };
+  // the lane's codes of the turn at k; a lane past K (the last turn may be short) gets zeros
+  auto load = [&](int64_t k, Codes* c) {
+    if (k + kg * 64 < p.K) {
 #pragma unroll
-      for (int i = 0; i < 64 / B; ++i) sv[i] = 0.0f;
-      const bool in = k0 < p.K;
-      if (in) {
-        w[0] = *reinterpret_cast<const v4u*>(q + k0 / 2);
-        w[1] = *reinterpret_cast<const v4u*>(q + k0 / 2 + 16);
-        if constexpr (LAYOUT == 2) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sv[i] = wscale<FMT>(s[(k0 / 16 + i) * (p.N / 16) + n0 / 16]);
+      for (int i = 0; i < TN; ++i) {
+        c[i].w[0] = *reinterpret_cast<const v4u*>(q[i] + k / 2);
+        c[i].w[1] = *reinterpret_cast<const v4u*>(q[i] + k / 2 + 16);
+        const uint8_t* s = sp[i] + k / B * t.s_k;
+        if (B == 32) {
+          c[i].s = *reinterpret_cast<const uint16_t*>(s);
+        } else if (t.s_k == 1) {
+          c[i].s = *reinterpret_cast<const uint32_t*>(s);
         } else {
-          const uint8_t* sp = LAYOUT == 1 ? s + (n0 / 16) * (p.K / 16) + k0 / 16 : s + nr * (p.K / B) + k0 / B;
-          if constexpr (B == 16) {
-            const uint32_t c = *reinterpret_cast<const uint32_t*>(sp);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sv[i] = wscale<FMT>((c >> (8 * i)) & 0xFFu);
-          } else {
-            const uint32_t c = *reinterpret_cast<const uint16_t*>(sp);
-            sv[0] = wscale<FMT>(c & 0xFFu);
-            sv[1] = wscale<FMT>(c >> 8);
-          }
+          c[i].s = s[0] | (uint32_t)s[t.s_k] << 8 | (uint32_t)s[2 * t.s_k] << 16 | (uint32_t)s[3 * t.s_k] << 24;
         }
       }
+    } else {
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        const v8bf b = decode8_bf16<FMT>(w[d >> 2][d & 3], sv[d * 8 / B]);
+      for (int i = 0; i < TN; ++i) c[i] = Codes{{v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}}, 0};
+    }
+  };
+
+  for (int64_t m0 = lo; m0 < hi; m0 += 16) {
+    v4f acc[TN];
 #pragma unroll
-        for (int t = 0; t < TM; ++t) {
-          const int64_t m = m0 + t * 16 + r;
-          const bool have = in && m < hi;
-          if constexpr (XF32) {
-            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (have) {
-              const v4f* xp = reinterpret_cast<const v4f*>(p.x + (m * p.ldx + k0 + d * 8) * 4);
-              const v4f a0 = xp[0], a1 = xp[1];
+    for (int i = 0; i < TN; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const char* xr = p.x + (min(m0 + r, hi - 1) * p.ldx + kg * 64) * 2;
+    int64_t k = (int64_t)wave * ROWS_K;
+    Codes next[TN];
+    load(k, next);
+    for (; k < p.K; k += ROWS_NW * ROWS_K) {
+      Codes c[TN];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                v[i] = a0[i];
-                v[4 + i] = a1[i];
-              }
-            }
-            v8bf part[3];
-            split3(v, part);
+      for (int i = 0; i < TN; ++i) c[i] = next[i];
+      if (k + ROWS_NW * ROWS_K < p.K) load(k + ROWS_NW * ROWS_K, next);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[i], b, acc[t], 0, 0, 0);
-          } else {
-            v4u a = {0, 0, 0, 0};
-            if (have) a = *reinterpret_cast<const v4u*>(p.x + (m * p.ldx + k0 + d * 8) * 2);
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), b, acc[t], 0, 0, 0);
-          }
+      for (int h = 0; h < 2; ++h) {
+        v4u x[PLANES][4];
+        if (k + kg * 64 < p.K) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int q = 0; q < PLANES; ++q)
+              x[q][d] = *reinterpret_cast<const v4u*>(xr + q * t.plane_bytes + (k + h * 32 + d * 8) * 2);
+        } else {
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int q = 0; q < PLANES; ++q) x[q][d] = v4u{0, 0, 0, 0};
         }
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int i = 0; i < TN; ++i) {
+            const float sv = code_value<E8>((c[i].s >> ((h * 4 + d) * 8 / B * 8)) & 0xFFu, t.scale_mul);
+            const v8bf b = decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(c[i].w[h][d], sv);
+#pragma unroll
+            for (int q = 0; q < PLANES; ++q)
+              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[q][d]), b, acc[i], 0, 0, 0);
+          }
       }
     }
 #pragma unroll
-    for (int t = 0; t < TM; ++t)
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[wave][t * 4 + i][lane] = acc[t][i];
+      for (int j = 0; j < 4; ++j) red[wave][i * 4 + j][lane] = acc[i][j];
     __syncthreads();
-    // output (m, n): lane 16 (m / 4 % 4) + n of register m % 4 of tile m / 16
-    for (int o = threadIdx.x; o < TM * 256; o += NW * 64) {
-      const int m = o >> 4, c = o & 15;
+    // output (m, n): lane 16 (m / 4) + n % 16 of register m % 4 of product n / 16
+    for (int o = threadIdx.x; o < TN * 256; o += ROWS_NW * 64) {
+      const int m = o / (16 * TN), c = o % (16 * TN);
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) v += red[w][(m >> 4) * 4 + (m & 3)][((m >> 2) & 3) * 16 + c];
+      for (int w = 0; w < ROWS_NW; ++w) v += red[w][(c >> 4) * 4 + (m & 3)][(m >> 2) * 16 + (c & 15)];
       const int64_t row = m0 + m, col = n0 + c;
       if (row < hi && col < p.N) {
-        const float g = p.g ? p.g[(int64_t)e * p.g_stride + (p.g_shift ? col >> p.g_shift : 0)] : 1.0f;
-        store1<YF32>(p.y, row * p.ldy + col, v * g);
+        if (p.g) v *= p.g[(int64_t)e * p.g_stride + (p.g_shift ? col >> p.g_shift : 0)];
+        t.y_f32 ? store1<true>(p.y, row * p.ldy + col, v) : store1<false>(p.y, row * p.ldy + col, v);
       }
     }
     __syncthreads();
@@ -304,14 +339,10 @@ struct TileMap {
 };
 
 struct TileArgs {
+  FormArgs f;
   uint32_t mtiles, ntiles;   // mtiles: an upper bound with offsets
-  int slices;            // parts of K, each with its own output rows in `part`
-  int64_t plane_bytes;   // bytes between the bf16 parts of float32 activations
-  bool y_f32, y_vec;     // y_vec: rows of y take 4-element stores
-  float* part;           // [slices][rows][N] sums of a split K, or null: write y
-  float scale_mul;       // 2^(127 - bias) of the 3-mantissa-bit scales
-  int64_t s_row, s_k;    // scale codes: bytes between rows (16-row bands for 2D) and between blocks of K
-  int s_band;            // log2 of the rows that share a scale row (0 or 4)
+  int slices;                // parts of K, each with its own output rows in `part`
+  float* part;               // [slices][rows][N] sums of a split K, or null: write y
 };
 
 // E8: power-of-two scales (block 32), else 3-mantissa-bit ones with block B. PLANES: bf16 parts of x.
@@ -340,7 +371,7 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
   if (p.offsets) map.find(p, mt, e, m0, m1);
   char* y = t.part ? reinterpret_cast<char*>(t.part + (int64_t)slice * p.rows * p.N) : p.y;
   const int64_t ldy = t.part ? p.N : p.ldy;
-  const bool y_f32 = t.part || t.y_f32;
+  const bool y_f32 = t.part || t.f.y_f32;
   if (p.offsets && e == p.n_experts) {   // the rows of dropped slots
     const int rows = (int)min((int64_t)BM, m1 - m0), cols = (int)min((int64_t)TILE_BN, p.N - n0);
     for (int i = threadIdx.x; i < rows * TILE_BN; i += TILE_NW * 64)
@@ -371,7 +402,7 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
       xsrc += ROWB;
     } else {
       const bool wrap = ++xplane == PLANES;
-      xsrc += wrap ? ROWB - (PLANES - 1) * t.plane_bytes : t.plane_bytes;
+      xsrc += wrap ? ROWB - (PLANES - 1) * t.f.plane_bytes : t.f.plane_bytes;
       xplane = wrap ? 0 : xplane;
     }
   };
@@ -385,7 +416,7 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
   for (int i = 0; i < TN; ++i) {
     const int64_t n = min(n0 + wave * OW + i * 32 + fr, p.N - 1);
     qp[i] = p.q + ((int64_t)e * p.N + n) * (p.K / 2) + (int64_t)k0 * (BK / 2) + fk * 16;
-    sp[i] = p.s + (int64_t)e * p.s_stride + (n >> t.s_band) * t.s_row + ((int64_t)k0 * 2 + fk) * NS * t.s_k;
+    sp[i] = p.s + (int64_t)e * p.s_stride + (n >> t.f.s_band) * t.f.s_row + ((int64_t)k0 * 2 + fk) * NS * t.f.s_k;
   }
   v4u codes[TN], cnext[TN];
   uint32_t sc[TN][NS], snext[TN][NS];
@@ -398,8 +429,8 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
       cnext[i] = *reinterpret_cast<const v4u*>(qp[i]);
       qp[i] += on * (BK / 2);
 #pragma unroll
-      for (int h = 0; h < NS; ++h) snext[i][h] = sp[i][h * t.s_k];
-      sp[i] += on * 2 * NS * t.s_k;
+      for (int h = 0; h < NS; ++h) snext[i][h] = sp[i][h * t.f.s_k];
+      sp[i] += on * 2 * NS * t.f.s_k;
     }
   };
   // The codes have landed (after wait_copies()): without this the compiler, which does not see that
@@ -420,12 +451,8 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
       for (int h = 0; h < NS; ++h) sc[i][h] = snext[i][h];
     }
   };
-  auto scale = [&](uint32_t c) {
-    // 3 mantissa bits: the code's bits as a float32 times 2^(127 - bias), subnormals included
-    return E8 ? wscale<FMT_E8M0>(c) : __uint_as_float(c << 20) * t.scale_mul;
-  };
   auto decode = [&](int i, int s) {   // dword s: k = 32 (lane / 32) + 8 s ..
-    const float sv = scale(sc[i][s * NS / 4]);
+    const float sv = code_value<E8>(sc[i][s * NS / 4], t.f.scale_mul);
     return decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(codes[i][s], sv);
   };
 
@@ -529,7 +556,7 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
       if (m >= m1 || n >= p.N) continue;
       const float gn = g ? g[p.g_shift ? n >> p.g_shift : 0] : 1.0f;   // stripes are multiples of 16 columns
       const int64_t at = m * ldy + n;
-      if (t.y_vec && n + 4 <= p.N) {
+      if (t.f.y_vec && n + 4 <= p.N) {
         if (y_f32) *reinterpret_cast<v4f*>(y + at * 4) = v4f{v[0] * gn, v[1] * gn, v[2] * gn, v[3] * gn};
         else *reinterpret_cast<uint64_t*>(y + at * 2) =
                  (uint64_t)pack_bf16(v[2] * gn, v[3] * gn) << 32 | pack_bf16(v[0] * gn, v[1] * gn);
@@ -579,8 +606,10 @@ __global__ __launch_bounds__(256) void k_zero_rows(char* y, int64_t rows, int64_
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Rows per expert (on average) from which the tile form is used.
-bool use_tile(const WLinearArgs& a) { return a.rows / a.n_experts > 16 && a.ldx <= (int64_t(1) << 22); }
+// Rows per expert (on average) from which the tile form is used; it keeps 32-bit offsets inside a tile.
+bool use_tile(const WLinearArgs& a) {
+  return a.rows / a.n_experts > 16 && a.ldx <= (int64_t(1) << 22) && a.K <= (int64_t(1) << 22);
+}
 
 struct TilePlan {
   int tm;          // 32-row products per tile
@@ -588,94 +617,73 @@ struct TilePlan {
   int slices;      // parts of K
 };
 
+// The tile height with the least rounds of tiles over the compute units times the time of a tile,
+// which is about that of its products and one more. Measured, 8192 rows 4096 -> 14336: 113, 61 and
+// 42 us a round for tm 8, 4 and 2; 2048 rows 4096 -> 6144: 118 us at 8 (192 tiles), 139 at 4 (384).
+// A K long enough is split where the tiles alone leave compute units idle.
 TilePlan plan_tiles(const WLinearArgs& a) {
-  TilePlan t;
-  const int64_t avg = a.rows / a.n_experts;
-  t.nt = div_up(a.N, TILE_BN);
-  t.tm = avg <= 32 ? 1 : avg <= 64 ? 2 : 4;
-  if (div_up(a.rows, 256) * t.nt >= 256) t.tm = 8;
-  t.mt = div_up(a.rows, t.tm * 32) + (a.offsets ? a.n_experts : 0);
-  const int64_t tiles = div_up(a.rows, t.tm * 32) * t.nt;
-  t.slices = (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, a.K / BK / 4));
-  return t;
+  const int64_t cus = device_cu_count(), groups = a.offsets_given ? a.n_experts : 0, ksteps = a.K / BK;
+  TilePlan best{};
+  double least = 0;
+  for (int tm : {8, 4, 2, 1}) {
+    TilePlan t;
+    t.tm = tm;
+    t.nt = div_up(a.N, TILE_BN);
+    t.mt = div_up(a.rows, tm * 32) + groups;
+    const int64_t tiles = (div_up(a.rows, tm * 32) + groups / 2) * t.nt;   // an expert's last tile is half full
+    t.slices = (int)std::max<int64_t>(1, std::min<int64_t>(cus / tiles, ksteps / 4));
+    const double cost = (double)div_up(tiles * t.slices, cus) * (tm + 1) / t.slices;
+    if (best.tm == 0 || cost < least) {
+      best = t;
+      least = cost;
+    }
+  }
+  return best;
 }
 
+// the bf16 parts of float32 activations, at the start of the workspace
 size_t planes_bytes(const WLinearArgs& a) { return a.x_f32 ? (size_t)div_up(3 * a.rows * a.K * 2, 256) * 256 : 0; }
 
 template <bool E8, int B, int PLANES>
-void launch_tile(const WLinearArgs& a, const WParams& p, const TileArgs& t, int tm) {
-  const uint32_t grid = (uint32_t)(div_up((int64_t)t.mtiles * t.ntiles * t.slices, 8) * 8);
-  if (tm == 1) k_wlinear_tile<E8, B, PLANES, 1, 4><<<grid, 256, 0, a.stream>>>(p, t);
-  else if (tm == 2) k_wlinear_tile<E8, B, PLANES, 2, 4><<<grid, 256, 0, a.stream>>>(p, t);
-  else if (tm == 4) k_wlinear_tile<E8, B, PLANES, 4, 4><<<grid, 256, 0, a.stream>>>(p, t);
-  else k_wlinear_tile<E8, B, PLANES, 8, 8><<<grid, 512, 0, a.stream>>>(p, t);
-}
-
-void run_tiles(const WLinearArgs& a, WParams p) {
-  const TilePlan plan = plan_tiles(a);
-  if (a.x_f32) {
-    const uint32_t grid = (uint32_t)std::min<int64_t>(div_up(a.rows * (a.K / 8), 256), 8192);
-    k_split3<<<grid, 256, 0, a.stream>>>((const float*)a.x, a.ldx, a.rows, a.K, (char*)a.ws);
-    p.x = (const char*)a.ws;
-    p.ldx = a.K;
+void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
+  if (!use_tile(a)) {
+    const uint32_t groups = a.offsets ? a.n_experts + 1 : 1;
+    // two products to an activation fragment, unless that leaves compute units without a workgroup
+    if (div_up(a.N, 32) * a.n_experts >= 2 * device_cu_count())
+      k_wlinear_rows<E8, B, PLANES, 2><<<dim3((uint32_t)div_up(a.N, 32), groups), ROWS_NW * 64, 0, a.stream>>>(p, f);
+    else
+      k_wlinear_rows<E8, B, PLANES, 1><<<dim3((uint32_t)div_up(a.N, 16), groups), ROWS_NW * 64, 0, a.stream>>>(p, f);
+    return;
   }
+  const TilePlan plan = plan_tiles(a);
   TileArgs t{};
+  t.f = f;
   t.mtiles = (uint32_t)plan.mt;
   t.ntiles = (uint32_t)plan.nt;
   t.slices = plan.slices;
-  t.plane_bytes = a.rows * a.K * 2;
-  t.y_f32 = a.y_f32;
-  if (plan.slices > 1) t.part = reinterpret_cast<float*>((char*)a.ws + planes_bytes(a));
-  const int64_t esz = t.part || a.y_f32 ? 4 : 2, ld = t.part ? a.N : a.ldy;
-  t.y_vec = (ld * esz) % (4 * esz) == 0 && (t.part || reinterpret_cast<uintptr_t>(a.y) % (4 * esz) == 0);
-  t.scale_mul = a.fmt == FMT_E4M3 ? 0x1p120f : 0x1p112f;
-  t.s_band = a.layout == 0 ? 0 : 4;
-  t.s_row = a.layout == 0 ? a.K / a.block : a.layout == 1 ? a.K / 16 : 1;
-  t.s_k = a.layout == 2 ? a.N / 16 : 1;
-  if (a.fmt == FMT_E8M0) a.x_f32 ? launch_tile<true, 32, 3>(a, p, t, plan.tm) : launch_tile<true, 32, 1>(a, p, t, plan.tm);
-  else if (a.block == 16) a.x_f32 ? launch_tile<false, 16, 3>(a, p, t, plan.tm) : launch_tile<false, 16, 1>(a, p, t, plan.tm);
-  else a.x_f32 ? launch_tile<false, 32, 3>(a, p, t, plan.tm) : launch_tile<false, 32, 1>(a, p, t, plan.tm);
+  if (plan.slices > 1) {
+    t.part = reinterpret_cast<float*>((char*)a.ws + planes_bytes(a));
+    t.f.y_vec = a.N % 4 == 0;
+  }
+  const uint32_t grid = (uint32_t)(div_up(plan.mt * plan.nt * plan.slices, 8) * 8);
+  if (plan.tm == 1) k_wlinear_tile<E8, B, PLANES, 1, 4><<<grid, 256, 0, a.stream>>>(p, t);
+  else if (plan.tm == 2) k_wlinear_tile<E8, B, PLANES, 2, 4><<<grid, 256, 0, a.stream>>>(p, t);
+  else if (plan.tm == 4) k_wlinear_tile<E8, B, PLANES, 4, 4><<<grid, 256, 0, a.stream>>>(p, t);
+  else k_wlinear_tile<E8, B, PLANES, 8, 8><<<grid, 512, 0, a.stream>>>(p, t);
   if (t.part) {
-    const uint32_t grid = (uint32_t)std::min<int64_t>(div_up(a.rows * a.N, 256), 4096);
-    if (a.y_f32) k_join_slices<true><<<grid, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
-    else k_join_slices<false><<<grid, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
+    const uint32_t join = (uint32_t)std::min<int64_t>(div_up(a.rows * a.N, 256), 4096);
+    if (a.y_f32) k_join_slices<true><<<join, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
+    else k_join_slices<false><<<join, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
   }
-}
-
-template <int FMT, int B, int LAYOUT, bool XF32, bool YF32>
-void launch(const WLinearArgs& a, const WParams& p) {
-  const dim3 grid((uint32_t)div_up(a.N, 16), (uint32_t)(a.offsets ? a.n_experts + 1 : 1));
-  const int64_t avg = a.rows / a.n_experts;
-  if (avg <= 16) k_wlinear_rows<FMT, B, LAYOUT, XF32, YF32, 1, 8><<<grid, 512, 0, a.stream>>>(p);
-  else k_wlinear_rows<FMT, B, LAYOUT, XF32, YF32, 4, 4><<<grid, 256, 0, a.stream>>>(p);
-}
-
-template <int FMT, int B, int LAYOUT>
-void by_types(const WLinearArgs& a, const WParams& p) {
-  if (a.x_f32) a.y_f32 ? launch<FMT, B, LAYOUT, true, true>(a, p) : launch<FMT, B, LAYOUT, true, false>(a, p);
-  else a.y_f32 ? launch<FMT, B, LAYOUT, false, true>(a, p) : launch<FMT, B, LAYOUT, false, false>(a, p);
-}
-
-template <int FMT>
-void by_layout(const WLinearArgs& a, const WParams& p) {
-  if constexpr (FMT != FMT_E8M0) {
-    if (a.block == 16) {
-      if (a.layout == 0) by_types<FMT, 16, 0>(a, p);
-      else if (a.layout == 1) by_types<FMT, 16, 1>(a, p);
-      else by_types<FMT, 16, 2>(a, p);
-      return;
-    }
-  }
-  by_types<FMT, 32, 0>(a, p);
 }
 
 }  // namespace
 
-// the tile form's bf16 parts of float32 activations and the sums of a split K
+// the bf16 parts of float32 activations and the sums of a split K
 size_t wlinear_ws(const WLinearArgs& a) {
-  if (!use_tile(a) || a.rows == 0 || a.N == 0 || a.K == 0) return 0;
-  const TilePlan t = plan_tiles(a);
-  return planes_bytes(a) + (t.slices > 1 ? (size_t)t.slices * a.rows * a.N * 4 : 0);
+  if (a.rows == 0 || a.N == 0 || a.K == 0) return 0;
+  const int slices = use_tile(a) ? plan_tiles(a).slices : 1;
+  return planes_bytes(a) + (slices > 1 ? (size_t)slices * a.rows * a.N * 4 : 0);
 }
 
 hipError_t run_wlinear(const WLinearArgs& a) {
@@ -702,10 +710,24 @@ hipError_t run_wlinear(const WLinearArgs& a) {
   p.ldy = a.ldy;
   p.s_stride = a.layout == 0 ? a.N * (a.K / a.block) : (a.N / 16) * (a.K / 16);
   p.g_stride = a.g_shift ? div_up(a.N, int64_t(1) << a.g_shift) : 1;
-  if (use_tile(a)) run_tiles(a, p);
-  else if (a.fmt == FMT_E8M0) by_layout<FMT_E8M0>(a, p);
-  else if (a.fmt == FMT_E4M3) by_layout<FMT_E4M3>(a, p);
-  else by_layout<FMT_UE5M3>(a, p);
+  FormArgs f{};
+  f.plane_bytes = a.rows * a.K * 2;
+  f.y_f32 = a.y_f32;
+  const int64_t esz = a.y_f32 ? 4 : 2;
+  f.y_vec = a.ldy % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * esz) == 0;
+  f.scale_mul = a.fmt == FMT_E4M3 ? 0x1p120f : 0x1p112f;
+  f.s_band = a.layout == 0 ? 0 : 4;
+  f.s_row = a.layout == 0 ? a.K / a.block : a.layout == 1 ? a.K / 16 : 1;
+  f.s_k = a.layout == 2 ? a.N / 16 : 1;
+  if (a.x_f32) {
+    const uint32_t grid = (uint32_t)std::min<int64_t>(div_up(a.rows * (a.K / 8), 256), 8192);
+    k_split3<<<grid, 256, 0, a.stream>>>((const float*)a.x, a.ldx, a.rows, a.K, (char*)a.ws);
+    p.x = (const char*)a.ws;
+    p.ldx = a.K;
+  }
+  if (a.fmt == FMT_E8M0) a.x_f32 ? launch<true, 32, 3>(a, p, f) : launch<true, 32, 1>(a, p, f);
+  else if (a.block == 16) a.x_f32 ? launch<false, 16, 3>(a, p, f) : launch<false, 16, 1>(a, p, f);
+  else a.x_f32 ? launch<false, 32, 3>(a, p, f) : launch<false, 32, 1>(a, p, f);
   return hipGetLastError();
 }
 
