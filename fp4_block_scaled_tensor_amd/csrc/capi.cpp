@@ -204,6 +204,7 @@ fp4_status gemm_common(const fp4_operand* a, const fp4_operand* b, float* c, int
 // ---- the mixture-of-experts operators (fp4bs_experts.h) ----
 constexpr int32_t MAX_EXPERTS = 1024;
 constexpr int64_t MAX_SLOTS = (int64_t(1) << 31) - 1;
+constexpr int64_t MAX_WIDTH = int64_t(1) << 22;   // K and ldx: 256 rows of either span less than 2^32 bytes
 
 fp4_status check_slots(int64_t tokens, int32_t topk, const char* what) {
   if (tokens < 0) return fail(FP4_EINVAL, "%s: negative size", what);
@@ -248,9 +249,9 @@ fp4_status check_wlinear(const fp4_operand* w, int64_t rows, int32_t x_dtype, in
   if ((st = check_operand(w, "weight")) != FP4_OK) return st;
   if (n_experts != 0 && (st = check_experts(n_experts, what)) != FP4_OK) return st;
   if (rows < 0) return fail(FP4_EINVAL, "%s: negative size", what);
-  if (rows > MAX_SLOTS || w->rows > (int64_t(1) << 31) || w->k > (int64_t(1) << 31))
-    return fail(FP4_EUNSUPPORTED, "%s: rows, N and K must be below 2^31", what);
-  if (w->block == 16 && w->rows > 0 && w->k > 0 && !aligned(w->s, 4))
+  if (rows > MAX_SLOTS || w->rows > MAX_SLOTS) return fail(FP4_EUNSUPPORTED, "%s: rows and N must be below 2^31", what);
+  if (w->k > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: K must be at most 2^22", what);
+  if (w->rows > 0 && w->k > 0 && !aligned(w->s, 4))
     return fail(FP4_EALIGN, "%s: scales not 4-byte aligned", what);
   a.x_f32 = x_dtype == FP4_IN_FP32;
   a.rows = rows;
@@ -278,6 +279,7 @@ fp4_status wlinear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx, co
   const int64_t esz = x_dtype == FP4_IN_FP32 ? 4 : 2, osz = y_dtype == FP4_IN_FP32 ? 4 : 2;
   if ((st = check_rows(x, ldx, w->k, esz, rows > 0 && w->k > 0, what, "x")) != FP4_OK) return st;
   if ((st = check_rows(y, ldy, w->rows, osz, rows > 0 && w->rows > 0, what, "y")) != FP4_OK) return st;
+  if (ldx > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: ldx must be at most 2^22", what);
   if (rows > 0 && w->k > 0 && (!aligned(x, 16) || (ldx * esz) % 16))
     return fail(FP4_EALIGN, "%s: rows of x must be 16-byte aligned", what);
   if (n_experts != 0 && (!offsets || !aligned(offsets, 4)))

@@ -29,6 +29,30 @@ __device__ __forceinline__ void dma16(const char* base, uint32_t off, char* dst)
       : "v"(off), "s"(base), "s"((uint32_t)reinterpret_cast<uintptr_t>(dst))
       : "memory", "m0");
 }
+// The same for one dword, or for one byte (zero-extended to a dword), per lane: LDS at dst + 4 * lane.
+__device__ __forceinline__ void dma4(const char* base, uint32_t off, char* dst) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 1\n\t"
+      "global_load_lds_dword %0, %1"
+      :
+      : "v"(off), "s"(base), "s"((uint32_t)reinterpret_cast<uintptr_t>(dst))
+      : "memory", "m0");
+}
+__device__ __forceinline__ void dma1(const char* base, uint32_t off, char* dst) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 1\n\t"
+      "global_load_lds_ubyte %0, %1"
+      :
+      : "v"(off), "s"(base), "s"((uint32_t)reinterpret_cast<uintptr_t>(dst))
+      : "memory", "m0");
+}
+// all but the newest N of the wave's copies have landed
+template <int N>
+__device__ __forceinline__ void wait_all_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// the wave's LDS reads are done
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 // a wave-uniform address, kept in scalar registers
 __device__ __forceinline__ const char* uniform_ptr(const char* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
@@ -146,17 +170,44 @@ __device__ __forceinline__ float code_value(uint32_t c, float scale_mul) {
 }
 
 // ---------------------------------------------------------------- rows form
-// For few activation rows the weight's bytes are the bound. A workgroup owns 16 TN weight rows (one
-// expert's, blockIdx.y) and the group's activation rows, 16 at a time; its eight waves take 256 k
-// each in turn, so that together they read 1 KiB of a row, and join their sums through LDS. Lane l
-// of a 16x16x32 product holds weight row l % 16 and eight consecutive k; its 64 codes of a turn are
-// 32 consecutive bytes of that row, and the next turn's are loaded before this one's are used.
-// Activation rows past the group read its last row: their products are not stored.
-constexpr int ROWS_NW = 8, ROWS_K = 256;
+// For few activation rows the weight's bytes are the bound, and what limits reading them is the
+// number of cache lines that the vector loads touch: lane l of a 16x16x32 product holds weight row
+// l % 16, so loads into that layout touch a line per lane, 64 of them for a kilobyte of codes or for
+// 64 bytes of scales (measured at 28672 x 4096, one row: 26 us with such loads, 18 us of it left
+// without the scales' loads). So everything goes through LDS, copied straight from global memory
+// with neighbouring lanes on neighbouring bytes, and is read from there in the products' layout.
+//
+// A workgroup owns 16 TN weight rows (one expert's, blockIdx.y) and the group's activation rows, 16
+// at a time. Its waves split K into contiguous parts and join their sums through LDS. A wave takes
+// 128 k a turn: 64 bytes of codes of each weight row, their scale codes and 256 bytes of each
+// activation row, into its own ring of D turns (no barrier; the copies of D - 1 turns are in flight
+// while one is multiplied). XR: activation rows that are copied (4 or 16); rows past the group
+// repeat its last one, and their products are not stored.
+//
+// Bank conflicts: codes row r (64 bytes) keeps its 16-byte piece j at j ^ (r / 4 % 4), activation
+// row r (256 bytes) at j ^ r % 16, so the 16 rows of a read fall on different banks.
+constexpr int ROWS_K = 128;
 
-template <bool E8, int B, int PLANES, int TN>
-__global__ __launch_bounds__(ROWS_NW * 64, PLANES == 1 ? 4 : 2) void k_wlinear_rows(WParams p, FormArgs t) {
-  __shared__ float red[ROWS_NW][TN * 4][64];
+template <bool E8_, int B_, int PLANES_, int TN_, int XR_, bool BYTES_>
+struct RowsForm {
+  static constexpr bool E8 = E8_, BYTES = BYTES_;
+  static constexpr int B = B_, PLANES = PLANES_, TN = TN_, XR = XR_;
+  static constexpr int NW = TN == 1 && PLANES == 1 ? 8 : 4;
+  // scale copies of a turn. Words: 8 bytes (block 16) or 4 (block 32) of each row, a dword a lane.
+  // Bytes: 8 of each 16-row band (transposed 2D scales) or 4 of each row, a byte a lane.
+  static constexpr int NSC = B == 16 ? (BYTES ? 1 : (TN * 32 + 63) / 64) : (BYTES ? TN : 1);
+  static constexpr int NXC = PLANES * XR / 4;
+  static constexpr int BATCH = TN + NSC + NXC;
+  static constexpr int SCALES = TN * 1024, XROWS = SCALES + NSC * 256, TURN = XROWS + NXC * 1024;
+  static constexpr int D = 3 * NW * TURN <= 80 * 1024 ? 3 : 2;
+  static_assert(TN * 1024 <= D * TURN, "the wave's sums fit its ring");
+};
+
+template <class F>
+__global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs t) {
+  constexpr bool E8 = F::E8, BYTES = F::BYTES;
+  constexpr int B = F::B, PLANES = F::PLANES, TN = F::TN, XR = F::XR, NW = F::NW, D = F::D;
+  __shared__ __attribute__((aligned(1024))) char lds[NW * D * F::TURN];
   const int e = blockIdx.y, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kg = lane >> 4;
   int64_t lo, hi;
@@ -164,100 +215,150 @@ __global__ __launch_bounds__(ROWS_NW * 64, PLANES == 1 ? 4 : 2) void k_wlinear_r
   if (lo >= hi) return;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * TN);
   if (p.offsets && e == p.n_experts) {   // the rows of dropped slots
-    for (int64_t i = threadIdx.x; i < (hi - lo) * (16 * TN); i += ROWS_NW * 64) {
+    for (int64_t i = threadIdx.x; i < (hi - lo) * (16 * TN); i += NW * 64) {
       const int64_t m = lo + i / (16 * TN), n = n0 + i % (16 * TN);
       if (n < p.N) t.y_f32 ? store1<true>(p.y, m * p.ldy + n, 0.0f) : store1<false>(p.y, m * p.ldy + n, 0.0f);
     }
     return;
   }
-  constexpr int NS = 64 / B;   // scale codes of a lane's 64 codes
-  const uint8_t* q[TN];
-  const uint8_t* sp[TN];
+  const int nlast = (int)min((int64_t)(16 * TN - 1), p.N - 1 - n0);   // rows past the weight repeat its last one
+  const int turns = (int)((p.K + ROWS_K - 1) / ROWS_K), span = (turns + NW - 1) / NW;
+  const int first = min(wave * span, turns - 1), mine = max(0, min(span, turns - wave * span));
+  const bool half = p.K % ROWS_K != 0;   // the last turn has only its first 64 k
+
+  // lane offsets of the copies
+  uint32_t qoff[TN], soff[F::NSC], xoff[XR / 4];
 #pragma unroll
   for (int i = 0; i < TN; ++i) {
-    const int64_t n = min(n0 + i * 16 + r, p.N - 1);   // rows past the weight read the last one and are not stored
-    q[i] = p.q + ((int64_t)e * p.N + n) * (p.K / 2) + kg * 32;
-    sp[i] = p.s + (int64_t)e * p.s_stride + (n >> t.s_band) * t.s_row + kg * NS * t.s_k;
+    const int row = i * 16 + (lane >> 2);
+    qoff[i] = (uint32_t)(min(row, nlast) * (int)(p.K / 2)) + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
   }
-  struct Codes {
-    v4u w[2];
-    uint32_t s;
-  };
-  // the lane's codes of the turn at k; a lane past K (the last turn may be short) gets zeros
-  auto load = [&](int64_t k, Codes* c) {
-    if (k + kg * 64 < p.K) {
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        c[i].w[0] = *reinterpret_cast<const v4u*>(q[i] + k / 2);
-        c[i].w[1] = *reinterpret_cast<const v4u*>(q[i] + k / 2 + 16);
-        const uint8_t* s = sp[i] + k / B * t.s_k;
-        if (B == 32) {
-          c[i].s = *reinterpret_cast<const uint16_t*>(s);
-        } else if (t.s_k == 1) {
-          c[i].s = *reinterpret_cast<const uint32_t*>(s);
-        } else {
-          c[i].s = s[0] | (uint32_t)s[t.s_k] << 8 | (uint32_t)s[2 * t.s_k] << 16 | (uint32_t)s[3 * t.s_k] << 24;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < TN; ++i) c[i] = Codes{{v4u{0, 0, 0, 0}, v4u{0, 0, 0, 0}}, 0};
-    }
-  };
+  for (int i = 0; i < F::NSC; ++i) {
+    const int per = B == 16 ? (BYTES ? 8 : 2) : (BYTES ? 4 : 1);   // lanes to a row (or band)
+    const int at = (i * 64 + lane) / per, row = B == 16 && BYTES ? min(at, TN - 1) * 16 : min(at, 16 * TN - 1);
+    const int64_t band = ((n0 + min(row, nlast)) >> t.s_band) - (n0 >> t.s_band);
+    soff[i] = (uint32_t)(band * t.s_row + (lane % per) * (BYTES ? t.s_k : 4));
+  }
+  const char* qbase = uniform_ptr(reinterpret_cast<const char*>(p.q + ((int64_t)e * p.N + n0) * (p.K / 2)));
+  const char* sbase =
+      uniform_ptr(reinterpret_cast<const char*>(p.s + (int64_t)e * p.s_stride + (n0 >> t.s_band) * t.s_row));
+  char* ring = lds + wave * (D * F::TURN);
+  const int64_t s_turn = ROWS_K / B * t.s_k;
 
   for (int64_t m0 = lo; m0 < hi; m0 += 16) {
+    const int mlast = (int)min(hi - 1 - m0, (int64_t)(XR - 1));
+#pragma unroll
+    for (int i = 0; i < XR / 4; ++i) {
+      const int row = i * 4 + (lane >> 4);
+      xoff[i] = (uint32_t)(min(row, mlast) * (int)(p.ldx * 2)) + (((lane & 15) ^ row) << 4);
+    }
+    const char* xbase = uniform_ptr(p.x + m0 * p.ldx * 2);
+    auto copy = [&](int i) {   // this wave's turn i
+      const int at = first + i;
+      const bool cut = half && at == turns - 1;
+      char* to = ring + (i % D) * F::TURN;
+      const char* src = qbase + (int64_t)at * (ROWS_K / 2);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        // pieces 2 and 3 of a short last turn lie past K: piece 0 or 1 instead (not used)
+        const int sw = ((j * 16 + (lane >> 2)) >> 2) & 3;
+        dma16(src, cut && (((lane & 3) ^ sw) & 2) ? qoff[j] - 32 : qoff[j], to + j * 1024);
+      }
+      src = sbase + at * s_turn;
+#pragma unroll
+      for (int j = 0; j < F::NSC; ++j) {
+        const int per = B == 16 ? (BYTES ? 8 : 2) : (BYTES ? 4 : 1);
+        if constexpr (BYTES) {
+          dma1(src, cut && (lane % per) >= per / 2 ? soff[j] - (uint32_t)(per / 2 * t.s_k) : soff[j], to + F::SCALES + j * 256);
+        } else {
+          dma4(src, cut && per == 2 && (lane & 1) ? soff[j] - 4 : soff[j], to + F::SCALES + j * 256);
+        }
+      }
+#pragma unroll
+      for (int o = 0; o < PLANES; ++o) {
+        src = xbase + o * t.plane_bytes + (int64_t)at * (ROWS_K * 2);
+#pragma unroll
+        for (int j = 0; j < XR / 4; ++j) {
+          const int piece = (lane & 15) ^ (j * 4 + (lane >> 4));
+          dma16(src, cut && (piece & 8) ? xoff[j] - 128 : xoff[j], to + F::XROWS + (o * (XR / 4) + j) * 1024);
+        }
+      }
+    };
+
     v4f acc[TN];
 #pragma unroll
     for (int i = 0; i < TN; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const char* xr = p.x + (min(m0 + r, hi - 1) * p.ldx + kg * 64) * 2;
-    int64_t k = (int64_t)wave * ROWS_K;
-    Codes next[TN];
-    load(k, next);
-    for (; k < p.K; k += ROWS_NW * ROWS_K) {
-      Codes c[TN];
 #pragma unroll
-      for (int i = 0; i < TN; ++i) c[i] = next[i];
-      if (k + ROWS_NW * ROWS_K < p.K) load(k + ROWS_NW * ROWS_K, next);
+    for (int i = 0; i < D; ++i)
+      if (i < mine) copy(i);
+    for (int i = 0; i < mine; ++i) {
+      if (D == 3 && i + 2 < mine) wait_all_but<2 * F::BATCH>();
+      else if (i + 1 < mine) wait_all_but<F::BATCH>();
+      else wait_all_but<0>();
+      const char* from = ring + (i % D) * F::TURN;
+      v4u w[TN], x[PLANES][4];
+      uint32_t sc[TN][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v4u x[PLANES][4];
-        if (k + kg * 64 < p.K) {
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-#pragma unroll
-            for (int q = 0; q < PLANES; ++q)
-              x[q][d] = *reinterpret_cast<const v4u*>(xr + q * t.plane_bytes + (k + h * 32 + d * 8) * 2);
+      for (int j = 0; j < TN; ++j) {
+        const int row = j * 16 + r;
+        w[j] = *reinterpret_cast<const v4u*>(from + row * 64 + ((kg ^ ((row >> 2) & 3)) << 4));
+        if constexpr (B == 16 && BYTES) {
+          sc[j][0] = *reinterpret_cast<const uint32_t*>(from + F::SCALES + (j * 8 + kg * 2) * 4);
+          sc[j][1] = *reinterpret_cast<const uint32_t*>(from + F::SCALES + (j * 8 + kg * 2 + 1) * 4);
+        } else if constexpr (B == 16) {
+          const uint32_t v = *reinterpret_cast<const uint16_t*>(from + F::SCALES + row * 8 + kg * 2);
+          sc[j][0] = v & 0xFFu;
+          sc[j][1] = v >> 8;
         } else {
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-#pragma unroll
-            for (int q = 0; q < PLANES; ++q) x[q][d] = v4u{0, 0, 0, 0};
+          sc[j][0] = sc[j][1] = *reinterpret_cast<const uint8_t*>(from + F::SCALES + (row * 4 + kg) * (BYTES ? 4 : 1));
         }
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-#pragma unroll
-          for (int i = 0; i < TN; ++i) {
-            const float sv = code_value<E8>((c[i].s >> ((h * 4 + d) * 8 / B * 8)) & 0xFFu, t.scale_mul);
-            const v8bf b = decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(c[i].w[h][d], sv);
-#pragma unroll
-            for (int q = 0; q < PLANES; ++q)
-              acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[q][d]), b, acc[i], 0, 0, 0);
-          }
       }
+#pragma unroll
+      for (int o = 0; o < PLANES; ++o)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int row = r % XR;
+          x[o][d] = *reinterpret_cast<const v4u*>(from + F::XROWS + o * (XR * 256) + row * 256 + (((kg * 4 + d) ^ row) << 4));
+        }
+      wait_lds();
+      if (i + D < mine) copy(i + D);
+      if (half && first + i == turns - 1 && kg >= 2) {   // past K
+#pragma unroll
+        for (int j = 0; j < TN; ++j) w[j] = v4u{0, 0, 0, 0};
+#pragma unroll
+        for (int o = 0; o < PLANES; ++o)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) x[o][d] = v4u{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const float sv = code_value<E8>(sc[j][d / 2], t.scale_mul);
+          const v8bf b = decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(w[j][d], sv);
+#pragma unroll
+          for (int o = 0; o < PLANES; ++o)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[o][d]), b, acc[j], 0, 0, 0);
+        }
     }
+    // the waves' sums, each in its own ring (its copies have landed and been read)
+    float* red = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) red[wave][i * 4 + j][lane] = acc[i][j];
+      for (int j = 0; j < 4; ++j) red[(i * 4 + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     // output (m, n): lane 16 (m / 4) + n % 16 of register m % 4 of product n / 16
-    for (int o = threadIdx.x; o < TN * 256; o += ROWS_NW * 64) {
+    const int rows = (int)min(hi - m0, (int64_t)16);
+    for (int o = threadIdx.x; o < rows * 16 * TN; o += NW * 64) {
       const int m = o / (16 * TN), c = o % (16 * TN);
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < ROWS_NW; ++w) v += red[w][(c >> 4) * 4 + (m & 3)][(m >> 2) * 16 + (c & 15)];
+      for (int w = 0; w < NW; ++w)
+        v += reinterpret_cast<const float*>(lds + w * (D * F::TURN))[((c >> 4) * 4 + (m & 3)) * 64 + (m >> 2) * 16 + (c & 15)];
       const int64_t row = m0 + m, col = n0 + c;
-      if (row < hi && col < p.N) {
+      if (col < p.N) {
         if (p.g) v *= p.g[(int64_t)e * p.g_stride + (p.g_shift ? col >> p.g_shift : 0)];
         t.y_f32 ? store1<true>(p.y, row * p.ldy + col, v) : store1<false>(p.y, row * p.ldy + col, v);
       }
@@ -606,10 +707,8 @@ __global__ __launch_bounds__(256) void k_zero_rows(char* y, int64_t rows, int64_
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Rows per expert (on average) from which the tile form is used; it keeps 32-bit offsets inside a tile.
-bool use_tile(const WLinearArgs& a) {
-  return a.rows / a.n_experts > 16 && a.ldx <= (int64_t(1) << 22) && a.K <= (int64_t(1) << 22);
-}
+// Rows per expert (on average) from which the tile form is used.
+bool use_tile(const WLinearArgs& a) { return a.rows / a.n_experts > 16; }
 
 struct TilePlan {
   int tm;          // 32-row products per tile
@@ -648,11 +747,30 @@ template <bool E8, int B, int PLANES>
 void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
   if (!use_tile(a)) {
     const uint32_t groups = a.offsets ? a.n_experts + 1 : 1;
-    // two products to an activation fragment, unless that leaves compute units without a workgroup
-    if (div_up(a.N, 32) * a.n_experts >= 2 * device_cu_count())
-      k_wlinear_rows<E8, B, PLANES, 2><<<dim3((uint32_t)div_up(a.N, 32), groups), ROWS_NW * 64, 0, a.stream>>>(p, f);
-    else
-      k_wlinear_rows<E8, B, PLANES, 1><<<dim3((uint32_t)div_up(a.N, 16), groups), ROWS_NW * 64, 0, a.stream>>>(p, f);
+    // as many products to an activation fragment as leave no compute unit without a workgroup
+    const int64_t cus = device_cu_count(), each = a.n_experts;
+    const int tn = PLANES == 1 && div_up(a.N, 64) * each >= cus ? 4 : div_up(a.N, 32) * each >= cus ? 2 : 1;
+    // scale codes byte by byte where a turn's are not aligned words
+    const bool bytes = f.s_k != 1 || (B == 32 && a.K % ROWS_K != 0);
+    auto go = [&](auto tn_, auto xr_, auto bytes_) {
+      using F = RowsForm<E8, B, PLANES, decltype(tn_)::value, decltype(xr_)::value, decltype(bytes_)::value>;
+      const dim3 grid((uint32_t)div_up(a.N, 16 * F::TN), groups);
+      k_wlinear_rows<F><<<grid, F::NW * 64, 0, a.stream>>>(p, f);
+    };
+    using std::integral_constant;
+    auto with_bytes = [&](auto tn_, auto xr_) { bytes ? go(tn_, xr_, std::true_type{}) : go(tn_, xr_, std::false_type{}); };
+    auto with_rows = [&](auto tn_) {
+      if constexpr (PLANES == 1) {
+        // four activation rows hold every group of a decode step with few sequences
+        if (a.rows <= 4) return with_bytes(tn_, integral_constant<int, 4>{});
+      }
+      with_bytes(tn_, integral_constant<int, 16>{});
+    };
+    if constexpr (PLANES == 1) {
+      if (tn == 4) return with_rows(integral_constant<int, 4>{});
+    }
+    if (tn == 2) with_rows(integral_constant<int, 2>{});
+    else with_rows(integral_constant<int, 1>{});
     return;
   }
   const TilePlan plan = plan_tiles(a);
