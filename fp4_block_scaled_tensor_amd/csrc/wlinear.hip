@@ -177,12 +177,12 @@ __device__ __forceinline__ float code_value(uint32_t c, float scale_mul) {
 // without the scales' loads). So everything goes through LDS, copied straight from global memory
 // with neighbouring lanes on neighbouring bytes, and is read from there in the products' layout.
 //
-// A workgroup owns 16 TN weight rows (one expert's, blockIdx.y) and the group's activation rows, 16
-// at a time. Its waves split K into contiguous parts and join their sums through LDS. A wave takes
+// A workgroup owns 16 TN weight rows (one expert's, blockIdx.y) and the group's activation rows, XR
+// (4, 8 or 16) at a time. Its waves split K into contiguous parts and join their sums through LDS. A wave takes
 // 128 k a turn: 64 bytes of codes of each weight row, their scale codes and 256 bytes of each
 // activation row, into its own ring of D turns (no barrier; the copies of D - 1 turns are in flight
-// while one is multiplied). XR: activation rows that are copied (4 or 16); rows past the group
-// repeat its last one, and their products are not stored.
+// while one is multiplied). Activation rows past the group repeat its last one; their products, and
+// those of the 16 - XR rows of a product that are not there, are not stored.
 //
 // Bank conflicts: codes row r (64 bytes) keeps its 16-byte piece j at j ^ (r / 4 % 4), activation
 // row r (256 bytes) at j ^ r % 16, so the 16 rows of a read fall on different banks.
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
   char* ring = lds + wave * (D * F::TURN);
   const int64_t s_turn = ROWS_K / B * t.s_k;
 
-  for (int64_t m0 = lo; m0 < hi; m0 += 16) {
+  for (int64_t m0 = lo; m0 < hi; m0 += XR) {
     const int mlast = (int)min(hi - 1 - m0, (int64_t)(XR - 1));
 #pragma unroll
     for (int i = 0; i < XR / 4; ++i) {
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
       for (int j = 0; j < 4; ++j) red[(i * 4 + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     // output (m, n): lane 16 (m / 4) + n % 16 of register m % 4 of product n / 16
-    const int rows = (int)min(hi - m0, (int64_t)16);
+    const int rows = (int)min(hi - m0, (int64_t)XR);
     for (int o = threadIdx.x; o < rows * 16 * TN; o += NW * 64) {
       const int m = o / (16 * TN), c = o % (16 * TN);
       float v = 0.0f;
@@ -759,10 +759,15 @@ void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
     };
     using std::integral_constant;
     auto with_bytes = [&](auto tn_, auto xr_) { bytes ? go(tn_, xr_, std::true_type{}) : go(tn_, xr_, std::false_type{}); };
+    // Activation rows at a time. An expert with more rows than that reads its weight again (from the
+    // caches); rows that are not there cost copies and LDS: 16 slots over 8 experts took 73 us with
+    // 16 rows at a time.
+    const int64_t avg = div_up(a.rows, a.n_experts);
+    const int xr = a.offsets ? (avg <= 2 ? 4 : avg <= 5 ? 8 : 16) : (avg <= 4 ? 4 : avg <= 8 ? 8 : 16);
     auto with_rows = [&](auto tn_) {
       if constexpr (PLANES == 1) {
-        // four activation rows hold every group of a decode step with few sequences
-        if (a.rows <= 4) return with_bytes(tn_, integral_constant<int, 4>{});
+        if (xr == 4) return with_bytes(tn_, integral_constant<int, 4>{});
+        if (xr == 8) return with_bytes(tn_, integral_constant<int, 8>{});
       }
       with_bytes(tn_, integral_constant<int, 16>{});
     };
