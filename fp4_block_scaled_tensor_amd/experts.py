@@ -7,12 +7,13 @@ the transposed weights -> expert_gather_grad. `linear` is the product with one w
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
 
 from . import _lib
-from . import QTensor, _dev_check, _in_dtype, _out_dtype, _stream
+from . import QTensor, _dev_check
 
 
 @dataclass
@@ -61,71 +62,113 @@ def stack_experts(weights: list[QTensor]) -> ExpertWeights:
                          torch.stack([t.g for t in weights]), w.fmt, w.block, w.layout, w.rows, w.k, w.g_stripe)
 
 
+# The calls below are short next to their launches, so the checks read each property once and the
+# workspace sizes, which depend on nothing but the sizes, are remembered by them.
+_DTYPES = {torch.bfloat16: _lib.FP4_IN_BF16, torch.float32: _lib.FP4_IN_FP32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of t's device."""
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+def _ld(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype) -> int:
+    """Checks a device matrix [rows, width] of dtype with unit column stride; its row stride (one
+    row's says nothing and is taken as its width)."""
+    if not t.is_cuda:
+        _dev_check(t)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != width:
+        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    stride = t.stride()
+    if width > 1 and stride[1] != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return stride[0] if rows > 1 else width
+
+
+def _width(name: str, t: torch.Tensor) -> int:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
+    return shape[1]
+
+
+@functools.lru_cache(maxsize=4096)
+def _sort_workspace(tokens: int, topk: int, n_experts: int) -> int:
+    ws = ctypes.c_size_t()
+    _lib.check(_lib.load().fp4_expert_sort_workspace(tokens, topk, n_experts, ctypes.byref(ws)))
+    return ws.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_workspace(rows: int, dtype: int, fmt: int, block: int, layout: int, g_stripe: int, n: int, k: int,
+                      n_experts: int) -> int:
+    ws = ctypes.c_size_t()
+    op = _lib.Operand(None, None, None, fmt, block, layout, g_stripe, n, k)
+    _lib.check(_lib.load().fp4_linear_workspace(rows, dtype, ctypes.byref(op), n_experts, ctypes.byref(ws)))
+    return ws.value
+
+
 def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
     """fp4_expert_sort: the plan of ids [tokens, topk] (int32 or int64; an id outside
     [0, n_experts) drops its slot)."""
     lib = _lib.load()
-    _dev_check(ids)
-    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("ids must be a 2-D int32 or int64 tensor")
-    if ids.shape[1] > 1 and ids.stride(1) != 1:
-        raise ValueError("ids must have unit column stride")
-    tokens, topk = ids.shape
+    topk = _width("ids", ids)
+    tokens = ids.shape[0]
+    ld = _ld("ids", ids, tokens, topk, ids.dtype)
     n, dev = tokens * topk, ids.device
-    ws = ctypes.c_size_t()
-    _lib.check(lib.fp4_expert_sort_workspace(tokens, topk, n_experts, ctypes.byref(ws)))
+    nb = _sort_workspace(tokens, topk, n_experts)
     order = torch.empty(n, dtype=torch.int32, device=dev)
     pos = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
     offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
-    work = torch.empty(ws.value, dtype=torch.uint8, device=dev) if ws.value else None
-    _lib.check(lib.fp4_expert_sort(ids.data_ptr(), int(ids.dtype == torch.int64), tokens, topk, _ld(ids), n_experts,
-                                   order.data_ptr(), pos.data_ptr(), offsets.data_ptr(),
-                                   work.data_ptr() if work is not None else None, ws.value, _stream()))
+    work = torch.empty(nb, dtype=torch.uint8, device=dev).data_ptr() if nb else None
+    _lib.check(lib.fp4_expert_sort(ids.data_ptr(), int(ids.dtype is torch.int64), tokens, topk, ld, n_experts,
+                                   order.data_ptr(), pos.data_ptr(), offsets.data_ptr(), work, nb, _stream_of(ids)))
     return ExpertPlan(order, pos, offsets, tokens, topk, n_experts)
-
-
-def _ld(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor; one row's stride says nothing and is taken as its width."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _rows_check(name: str, t: torch.Tensor, rows: int, width: int | None, dtype=None) -> None:
-    if t.dim() != 2 or t.shape[0] != rows or (width is not None and t.shape[1] != width):
-        raise ValueError(f"{name} must be [{rows}, {'hidden' if width is None else width}], got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-
-
-def _out(out, rows, width, dtype, dev) -> torch.Tensor:
-    if out is None:
-        return torch.empty((rows, width), dtype=dtype, device=dev)
-    _dev_check(out)
-    _rows_check("out", out, rows, width, dtype)
-    return out
 
 
 def expert_gather(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_gather: token rows [tokens, hidden] in expert order, [tokens * topk, hidden];
     dropped slots give zero rows."""
     lib = _lib.load()
-    _dev_check(x)
-    _rows_check("x", x, plan.tokens, None)
-    out = _out(out, plan.tokens * plan.topk, x.shape[1], x.dtype, x.device)
-    _lib.check(lib.fp4_expert_gather(x.data_ptr(), _in_dtype(x), plan.tokens, x.shape[1], _ld(x), plan.pos.data_ptr(),
-                                     plan.topk, out.data_ptr(), _ld(out), _stream()))
+    h, n = _width("x", x), plan.tokens * plan.topk
+    ldx = _ld("x", x, plan.tokens, h, x.dtype)
+    dt = _dtype(x, "x")
+    if out is None:
+        out, ldo = x.new_empty((n, h)), h
+    else:
+        ldo = _ld("out", out, n, h, x.dtype)
+    _lib.check(lib.fp4_expert_gather(x.data_ptr(), dt, plan.tokens, h, ldx, plan.pos.data_ptr(), plan.topk,
+                                     out.data_ptr(), ldo, _stream_of(x)))
     return out
 
 
 def expert_gather_grad(dxs: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_gather_grad: each token's sum [tokens, hidden] of its kept slots' rows."""
     lib = _lib.load()
-    _dev_check(dxs)
-    _rows_check("dxs", dxs, plan.tokens * plan.topk, None)
-    out = _out(out, plan.tokens, dxs.shape[1], dxs.dtype, dxs.device)
-    _lib.check(lib.fp4_expert_gather_grad(dxs.data_ptr(), _in_dtype(dxs), plan.tokens, dxs.shape[1], _ld(dxs),
-                                          plan.pos.data_ptr(), plan.topk, out.data_ptr(), _ld(out), _stream()))
+    h = _width("dxs", dxs)
+    ld = _ld("dxs", dxs, plan.tokens * plan.topk, h, dxs.dtype)
+    dt = _dtype(dxs, "dxs")
+    if out is None:
+        out, ldo = dxs.new_empty((plan.tokens, h)), h
+    else:
+        ldo = _ld("out", out, plan.tokens, h, dxs.dtype)
+    _lib.check(lib.fp4_expert_gather_grad(dxs.data_ptr(), dt, plan.tokens, h, ld, plan.pos.data_ptr(), plan.topk,
+                                          out.data_ptr(), ldo, _stream_of(dxs)))
     return out
 
 
@@ -134,13 +177,16 @@ def expert_combine(ys: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     """fp4_expert_combine: each token's weighted sum [tokens, hidden] of its kept slots' rows ys
     [tokens * topk, hidden]; weights float32 [tokens, topk]."""
     lib = _lib.load()
-    _dev_check(ys, weights)
-    _rows_check("ys", ys, plan.tokens * plan.topk, None)
-    _rows_check("weights", weights, plan.tokens, plan.topk, torch.float32)
-    out = _out(out, plan.tokens, ys.shape[1], ys.dtype, ys.device)
-    _lib.check(lib.fp4_expert_combine(ys.data_ptr(), _in_dtype(ys), plan.tokens, ys.shape[1], _ld(ys),
-                                      weights.data_ptr(), _ld(weights), plan.pos.data_ptr(), plan.topk,
-                                      out.data_ptr(), _ld(out), _stream()))
+    h = _width("ys", ys)
+    ld = _ld("ys", ys, plan.tokens * plan.topk, h, ys.dtype)
+    ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32)
+    dt = _dtype(ys, "ys")
+    if out is None:
+        out, ldo = ys.new_empty((plan.tokens, h)), h
+    else:
+        ldo = _ld("out", out, plan.tokens, h, ys.dtype)
+    _lib.check(lib.fp4_expert_combine(ys.data_ptr(), dt, plan.tokens, h, ld, weights.data_ptr(), ldw,
+                                      plan.pos.data_ptr(), plan.topk, out.data_ptr(), ldo, _stream_of(ys)))
     return out
 
 
@@ -148,24 +194,32 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
     """fp4_expert_combine_grad: (dys [tokens * topk, hidden] of ys's dtype, dweights float32
     [tokens, topk]) for dy [tokens, hidden]."""
     lib = _lib.load()
-    _dev_check(dy, ys, weights)
-    n, dev = plan.tokens * plan.topk, dy.device
-    _rows_check("dy", dy, plan.tokens, None)
-    _rows_check("ys", ys, n, dy.shape[1], dy.dtype)
-    _rows_check("weights", weights, plan.tokens, plan.topk, torch.float32)
-    dys = torch.empty((n, dy.shape[1]), dtype=dy.dtype, device=dev)
-    dw = torch.empty((plan.tokens, plan.topk), dtype=torch.float32, device=dev)
-    _lib.check(lib.fp4_expert_combine_grad(dy.data_ptr(), _in_dtype(dy), plan.tokens, dy.shape[1], _ld(dy),
-                                           ys.data_ptr(), _ld(ys), weights.data_ptr(), _ld(weights),
-                                           plan.pos.data_ptr(), plan.topk, dys.data_ptr(), _ld(dys), dw.data_ptr(),
-                                           plan.topk, _stream()))
+    h, n = _width("dy", dy), plan.tokens * plan.topk
+    lddy = _ld("dy", dy, plan.tokens, h, dy.dtype)
+    ldys = _ld("ys", ys, n, h, dy.dtype)
+    ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32)
+    dt = _dtype(dy, "dy")
+    dys = dy.new_empty((n, h))
+    dw = weights.new_empty((plan.tokens, plan.topk))
+    _lib.check(lib.fp4_expert_combine_grad(dy.data_ptr(), dt, plan.tokens, h, lddy, ys.data_ptr(), ldys,
+                                           weights.data_ptr(), ldw, plan.pos.data_ptr(), plan.topk, dys.data_ptr(), h,
+                                           dw.data_ptr(), plan.topk, _stream_of(dy)))
     return dys, dw
 
 
-def _workspace(lib, rows: int, dt: int, op, n_experts: int, dev):
-    ws = ctypes.c_size_t()
-    _lib.check(lib.fp4_linear_workspace(rows, dt, ctypes.byref(op), n_experts, ctypes.byref(ws)))
-    return (torch.empty(ws.value, dtype=torch.uint8, device=dev) if ws.value else None), ws.value
+def _product(x, w, rows, n_experts, out_dtype, out):
+    """What linear and expert_linear share: checks, output, workspace."""
+    ldx = _ld("x", x, rows, w.k, x.dtype)
+    dt = _dtype(x, "x")
+    if out is None:
+        out = x.new_empty((rows, w.rows)) if out_dtype is None else x.new_empty((rows, w.rows), dtype=out_dtype)
+        ldo = w.rows
+    else:
+        ldo = _ld("out", out, rows, w.rows, out_dtype or out.dtype)
+    odt = _dtype(out, "out")
+    nb = _linear_workspace(rows, dt, w.fmt, w.block, w.layout, w.g_stripe, w.rows, w.k, n_experts)
+    ws = x.new_empty(nb, dtype=torch.uint8).data_ptr() if nb else None
+    return ldx, dt, out, ldo, odt, ws, nb
 
 
 def linear(x: torch.Tensor, w: QTensor, out_dtype=None, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -173,15 +227,13 @@ def linear(x: torch.Tensor, w: QTensor, out_dtype=None, out: torch.Tensor | None
     transposed, [rows, n] in out_dtype (x's by default). The transposed operand of a TILE2D weight
     gives the gradient dX = dY . W."""
     lib = _lib.load()
-    _dev_check(x, w.q)
-    if x.dim() != 2 or x.shape[1] != w.k or x.stride(1) != 1:
-        raise ValueError(f"x must be [rows, {w.k}] with unit column stride, got {tuple(x.shape)}")
-    dt = _in_dtype(x)
-    out = _out(out, x.shape[0], w.rows, out_dtype or (x.dtype if out is None else out.dtype), x.device)
+    _width("x", x)
+    rows = x.shape[0]
+    ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, 0, out_dtype, out)
+    _dev_check(w.q)
     op = w.operand()
-    ws, nb = _workspace(lib, x.shape[0], dt, op, 0, x.device)
-    _lib.check(lib.fp4_linear(x.data_ptr(), dt, x.shape[0], _ld(x), ctypes.byref(op), out.data_ptr(),
-                              _out_dtype(out.dtype), _ld(out), ws.data_ptr() if nb else None, nb, _stream()))
+    _lib.check(lib.fp4_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), out.data_ptr(), odt, ldo, ws, nb,
+                              _stream_of(x)))
     return out
 
 
@@ -192,16 +244,14 @@ def expert_linear(x: torch.Tensor, w: ExpertWeights, plan: ExpertPlan | torch.Te
     [n_experts + 1] on the device); rows past the last offset give zeros."""
     lib = _lib.load()
     offsets = plan.offsets if isinstance(plan, ExpertPlan) else plan
-    _dev_check(x, w.q, offsets)
-    if x.dim() != 2 or x.shape[1] != w.k or x.stride(1) != 1:
-        raise ValueError(f"x must be [rows, {w.k}] with unit column stride, got {tuple(x.shape)}")
-    if offsets.dtype != torch.int32 or offsets.shape != (w.n_experts + 1,) or not offsets.is_contiguous():
-        raise ValueError(f"offsets must be a contiguous int32 tensor of {w.n_experts + 1} elements")
-    dt = _in_dtype(x)
-    out = _out(out, x.shape[0], w.rows, out_dtype or (x.dtype if out is None else out.dtype), x.device)
+    experts = w.n_experts
+    if offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 tensor of {experts + 1} elements")
+    _width("x", x)
+    rows = x.shape[0]
+    ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, experts, out_dtype, out)
+    _dev_check(w.q, offsets)
     op = w.operand()
-    ws, nb = _workspace(lib, x.shape[0], dt, op, w.n_experts, x.device)
-    _lib.check(lib.fp4_expert_linear(x.data_ptr(), dt, x.shape[0], _ld(x), ctypes.byref(op), w.n_experts,
-                                     offsets.data_ptr(), out.data_ptr(), _out_dtype(out.dtype), _ld(out),
-                                     ws.data_ptr() if nb else None, nb, _stream()))
+    _lib.check(lib.fp4_expert_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), experts, offsets.data_ptr(),
+                                     out.data_ptr(), odt, ldo, ws, nb, _stream_of(x)))
     return out

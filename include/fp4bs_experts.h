@@ -102,7 +102,7 @@ fp4_status fp4_linear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx,
 fp4_status fp4_expert_linear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx, const fp4_operand* w,
                              int32_t n_experts, const int32_t* offsets, void* y, int32_t y_dtype, int64_t ldy,
                              void* ws, size_t ws_bytes, void* stream);
-/* Bytes of ws for either call (n_experts 0: fp4_linear). */
+/* Bytes of ws for either call (n_experts 0: fp4_linear), from the sizes alone: w's pointers are not looked at. */
 fp4_status fp4_linear_workspace(int64_t rows, int32_t x_dtype, const fp4_operand* w, int32_t n_experts,
                                 size_t* ws_bytes);
 
