@@ -169,36 +169,107 @@ __device__ __forceinline__ float code_value(uint32_t c, float scale_mul) {
   return E8 ? wscale<FMT_E8M0>(c) : __uint_as_float(c << 20) * scale_mul;
 }
 
-// ---------------------------------------------------------------- rows form
-// For few activation rows the weight's bytes are the bound, and what limits reading them is the
-// number of cache lines that the vector loads touch: lane l of a 16x16x32 product holds weight row
-// l % 16, so loads into that layout touch a line per lane, 64 of them for a kilobyte of codes or for
-// 64 bytes of scales (measured at 28672 x 4096, one row: 26 us with such loads, 18 us of it left
-// without the scales' loads). So everything goes through LDS, copied straight from global memory
-// with neighbouring lanes on neighbouring bytes, and is read from there in the products' layout.
+// ---------------------------------------------------------------- weight turns
+// What limits reading a weight is the number of cache lines that the vector loads touch: lane l of a
+// matrix product holds weight row l % 16 (or l % 32), so loads into that layout touch a line per
+// lane, 64 of them for a kilobyte of codes or for 64 bytes of scales (measured at 28672 x 4096, one
+// activation row: 26 us with such loads, 18 us with the scales' left out). So codes and scales are
+// copied straight from global memory into LDS with neighbouring lanes on neighbouring bytes, a turn
+// of 128 k at a time and each wave its own rows (no barrier), and read from there in the products'
+// layout.
 //
-// A workgroup owns 16 TN weight rows (one expert's, blockIdx.y) and the group's activation rows, XR
-// (4, 8 or 16) at a time. Its waves split K into contiguous parts and join their sums through LDS. A wave takes
-// 128 k a turn: 64 bytes of codes of each weight row, their scale codes and 256 bytes of each
-// activation row, into its own ring of D turns (no barrier; the copies of D - 1 turns are in flight
-// while one is multiplied). Activation rows past the group repeat its last one; their products, and
-// those of the 16 - XR rows of a product that are not there, are not stored.
-//
-// Bank conflicts: codes row r (64 bytes) keeps its 16-byte piece j at j ^ (r / 4 % 4), activation
-// row r (256 bytes) at j ^ r % 16, so the 16 rows of a read fall on different banks.
-constexpr int ROWS_K = 128;
+// A turn of 16 G rows: 64 bytes of codes of each row, then the scale codes. Words: 8 bytes (block
+// 16) or 4 (block 32) of each row, a dword a lane. BYTES: 8 of each 16-row band (transposed 2D
+// scales) or 4 of each row (block 32 with rows that are not whole words), a byte a lane and kept in
+// a dword. Codes row r keeps its 16-byte piece j at j ^ (r / 4 % 4), so that the 16 rows of a read
+// fall on different banks.
+constexpr int TURN_K = 128;
 
+template <int B, bool BYTES, int G>
+struct WeightTurns {
+  static constexpr int PER = B == 16 ? (BYTES ? 8 : 2) : (BYTES ? 4 : 1);   // lanes to a row's (band's) scales
+  static constexpr int NSC = B == 16 ? (BYTES ? 1 : (G * 32 + 63) / 64) : (BYTES ? G : (G * 16 + 63) / 64);
+  static constexpr int COPIES = G + NSC, SCALES = G * 1024, SIZE = SCALES + NSC * 256;
+  uint32_t qoff[G], soff[NSC];
+  const char *qbase, *sbase;
+  int64_t s_turn;
+  bool half;     // the weight's last turn has only its first 64 k
+  int last;      // that turn
+
+  // rows n0 (a multiple of 16, below N) .. of expert e; rows past the weight repeat its last one
+  __device__ __forceinline__ void init(const WParams& p, const FormArgs& t, int e, int64_t n0) {
+    const int lane = threadIdx.x & 63, nlast = (int)min((int64_t)(16 * G - 1), p.N - 1 - n0);
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int row = i * 16 + (lane >> 2);
+      qoff[i] = (uint32_t)(min(row, nlast) * (int)(p.K / 2)) + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < NSC; ++i) {
+      const int at = (i * 64 + lane) / PER, row = B == 16 && BYTES ? min(at, G - 1) * 16 : min(at, 16 * G - 1);
+      const int64_t band = ((n0 + min(row, nlast)) >> t.s_band) - (n0 >> t.s_band);
+      soff[i] = (uint32_t)(band * t.s_row + (lane % PER) * (BYTES ? t.s_k : 4));
+    }
+    qbase = uniform_ptr(reinterpret_cast<const char*>(p.q + ((int64_t)e * p.N + n0) * (p.K / 2)));
+    sbase = uniform_ptr(reinterpret_cast<const char*>(p.s + (int64_t)e * p.s_stride + (n0 >> t.s_band) * t.s_row));
+    s_turn = TURN_K / B * t.s_k;
+    half = p.K % TURN_K != 0;
+    last = (int)((p.K + TURN_K - 1) / TURN_K) - 1;
+  }
+  __device__ __forceinline__ void copy(int turn, char* to) const {
+    const int lane = threadIdx.x & 63;
+    const bool cut = half && turn == last;   // what lies past K: the 64 k before it instead (not used)
+    const char* src = qbase + (int64_t)turn * (TURN_K / 2);
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      const int piece = (lane & 3) ^ (((j * 16 + (lane >> 2)) >> 2) & 3);
+      dma16(src, cut && (piece & 2) ? qoff[j] - 32 : qoff[j], to + j * 1024);
+    }
+    src = sbase + turn * s_turn;
+#pragma unroll
+    for (int j = 0; j < NSC; ++j) {
+      const uint32_t step = BYTES ? (uint32_t)(s_turn / 2) : 4;
+      const uint32_t off = cut && PER > 1 && (lane % PER) >= PER / 2 ? soff[j] - step : soff[j];
+      if constexpr (BYTES) dma1(src, off, to + SCALES + j * 256);
+      else dma4(src, off, to + SCALES + j * 256);
+    }
+  }
+  // the 32 codes of piece j (32 k) of a row, and their scale codes (two at block 16)
+  static __device__ __forceinline__ v4u codes(const char* turn, int row, int j) {
+    return *reinterpret_cast<const v4u*>(turn + row * 64 + ((j ^ ((row >> 2) & 3)) << 4));
+  }
+  static __device__ __forceinline__ void scales(const char* turn, int row, int j, uint32_t* sc) {
+    const char* s = turn + SCALES;
+    if constexpr (B == 16 && BYTES) {
+      sc[0] = *reinterpret_cast<const uint32_t*>(s + ((row >> 4) * 8 + j * 2) * 4);
+      sc[1] = *reinterpret_cast<const uint32_t*>(s + ((row >> 4) * 8 + j * 2 + 1) * 4);
+    } else if constexpr (B == 16) {
+      const uint32_t v = *reinterpret_cast<const uint16_t*>(s + row * 8 + j * 2);
+      sc[0] = v & 0xFFu;
+      sc[1] = v >> 8;
+    } else {
+      sc[0] = sc[1] = *reinterpret_cast<const uint8_t*>(s + (row * 4 + j) * (BYTES ? 4 : 1));
+    }
+  }
+};
+
+// ---------------------------------------------------------------- rows form
+// For few activation rows the weight's bytes are the bound. A workgroup owns 16 TN weight rows (one
+// expert's, blockIdx.y) and the group's activation rows, XR (4, 8 or 16) at a time. Its waves split
+// K into contiguous parts and join their sums through LDS. A wave takes a turn of its weight rows
+// and 256 bytes of each activation row at a time into its own ring of D turns: the copies of D - 1
+// turns are in flight while one is multiplied. Activation rows past the group repeat its last one;
+// their products, and those of the 16 - XR rows of a product that are not there, are not stored.
+// Activation row r (256 bytes) keeps its 16-byte piece j at j ^ r % 16, against bank conflicts.
 template <bool E8_, int B_, int PLANES_, int TN_, int XR_, bool BYTES_>
 struct RowsForm {
   static constexpr bool E8 = E8_, BYTES = BYTES_;
   static constexpr int B = B_, PLANES = PLANES_, TN = TN_, XR = XR_;
+  using Weight = WeightTurns<B, BYTES, TN>;
   static constexpr int NW = TN == 1 && PLANES == 1 ? 8 : 4;
-  // scale copies of a turn. Words: 8 bytes (block 16) or 4 (block 32) of each row, a dword a lane.
-  // Bytes: 8 of each 16-row band (transposed 2D scales) or 4 of each row, a byte a lane.
-  static constexpr int NSC = B == 16 ? (BYTES ? 1 : (TN * 32 + 63) / 64) : (BYTES ? TN : 1);
-  static constexpr int NXC = PLANES * XR / 4;
-  static constexpr int BATCH = TN + NSC + NXC;
-  static constexpr int SCALES = TN * 1024, XROWS = SCALES + NSC * 256, TURN = XROWS + NXC * 1024;
+  static constexpr int NXC = PLANES * XR / 4;   // copies of activation rows
+  static constexpr int BATCH = Weight::COPIES + NXC;
+  static constexpr int XROWS = Weight::SIZE, TURN = XROWS + NXC * 1024;
   static constexpr int D = 3 * NW * TURN <= 80 * 1024 ? 3 : 2;
   static_assert(TN * 1024 <= D * TURN, "the wave's sums fit its ring");
 };
@@ -221,30 +292,12 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
     }
     return;
   }
-  const int nlast = (int)min((int64_t)(16 * TN - 1), p.N - 1 - n0);   // rows past the weight repeat its last one
-  const int turns = (int)((p.K + ROWS_K - 1) / ROWS_K), span = (turns + NW - 1) / NW;
+  const int turns = (int)((p.K + TURN_K - 1) / TURN_K), span = (turns + NW - 1) / NW;
   const int first = min(wave * span, turns - 1), mine = max(0, min(span, turns - wave * span));
-  const bool half = p.K % ROWS_K != 0;   // the last turn has only its first 64 k
-
-  // lane offsets of the copies
-  uint32_t qoff[TN], soff[F::NSC], xoff[XR / 4];
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int row = i * 16 + (lane >> 2);
-    qoff[i] = (uint32_t)(min(row, nlast) * (int)(p.K / 2)) + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
-  }
-#pragma unroll
-  for (int i = 0; i < F::NSC; ++i) {
-    const int per = B == 16 ? (BYTES ? 8 : 2) : (BYTES ? 4 : 1);   // lanes to a row (or band)
-    const int at = (i * 64 + lane) / per, row = B == 16 && BYTES ? min(at, TN - 1) * 16 : min(at, 16 * TN - 1);
-    const int64_t band = ((n0 + min(row, nlast)) >> t.s_band) - (n0 >> t.s_band);
-    soff[i] = (uint32_t)(band * t.s_row + (lane % per) * (BYTES ? t.s_k : 4));
-  }
-  const char* qbase = uniform_ptr(reinterpret_cast<const char*>(p.q + ((int64_t)e * p.N + n0) * (p.K / 2)));
-  const char* sbase =
-      uniform_ptr(reinterpret_cast<const char*>(p.s + (int64_t)e * p.s_stride + (n0 >> t.s_band) * t.s_row));
+  typename F::Weight weight;
+  weight.init(p, t, e, n0);
   char* ring = lds + wave * (D * F::TURN);
-  const int64_t s_turn = ROWS_K / B * t.s_k;
+  uint32_t xoff[XR / 4];
 
   for (int64_t m0 = lo; m0 < hi; m0 += XR) {
     const int mlast = (int)min(hi - 1 - m0, (int64_t)(XR - 1));
@@ -255,29 +308,12 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
     }
     const char* xbase = uniform_ptr(p.x + m0 * p.ldx * 2);
     auto copy = [&](int i) {   // this wave's turn i
-      const int at = first + i;
-      const bool cut = half && at == turns - 1;
       char* to = ring + (i % D) * F::TURN;
-      const char* src = qbase + (int64_t)at * (ROWS_K / 2);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        // pieces 2 and 3 of a short last turn lie past K: piece 0 or 1 instead (not used)
-        const int sw = ((j * 16 + (lane >> 2)) >> 2) & 3;
-        dma16(src, cut && (((lane & 3) ^ sw) & 2) ? qoff[j] - 32 : qoff[j], to + j * 1024);
-      }
-      src = sbase + at * s_turn;
-#pragma unroll
-      for (int j = 0; j < F::NSC; ++j) {
-        const int per = B == 16 ? (BYTES ? 8 : 2) : (BYTES ? 4 : 1);
-        if constexpr (BYTES) {
-          dma1(src, cut && (lane % per) >= per / 2 ? soff[j] - (uint32_t)(per / 2 * t.s_k) : soff[j], to + F::SCALES + j * 256);
-        } else {
-          dma4(src, cut && per == 2 && (lane & 1) ? soff[j] - 4 : soff[j], to + F::SCALES + j * 256);
-        }
-      }
+      weight.copy(first + i, to);
+      const bool cut = weight.half && first + i == weight.last;
 #pragma unroll
       for (int o = 0; o < PLANES; ++o) {
-        src = xbase + o * t.plane_bytes + (int64_t)at * (ROWS_K * 2);
+        const char* src = xbase + o * t.plane_bytes + (int64_t)(first + i) * (TURN_K * 2);
 #pragma unroll
         for (int j = 0; j < XR / 4; ++j) {
           const int piece = (lane & 15) ^ (j * 4 + (lane >> 4));
@@ -301,18 +337,8 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
       uint32_t sc[TN][2];
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const int row = j * 16 + r;
-        w[j] = *reinterpret_cast<const v4u*>(from + row * 64 + ((kg ^ ((row >> 2) & 3)) << 4));
-        if constexpr (B == 16 && BYTES) {
-          sc[j][0] = *reinterpret_cast<const uint32_t*>(from + F::SCALES + (j * 8 + kg * 2) * 4);
-          sc[j][1] = *reinterpret_cast<const uint32_t*>(from + F::SCALES + (j * 8 + kg * 2 + 1) * 4);
-        } else if constexpr (B == 16) {
-          const uint32_t v = *reinterpret_cast<const uint16_t*>(from + F::SCALES + row * 8 + kg * 2);
-          sc[j][0] = v & 0xFFu;
-          sc[j][1] = v >> 8;
-        } else {
-          sc[j][0] = sc[j][1] = *reinterpret_cast<const uint8_t*>(from + F::SCALES + (row * 4 + kg) * (BYTES ? 4 : 1));
-        }
+        w[j] = F::Weight::codes(from, j * 16 + r, kg);
+        F::Weight::scales(from, j * 16 + r, kg, sc[j]);
       }
 #pragma unroll
       for (int o = 0; o < PLANES; ++o)
@@ -323,7 +349,7 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
         }
       wait_lds();
       if (i + D < mine) copy(i + D);
-      if (half && first + i == turns - 1 && kg >= 2) {   // past K
+      if (weight.half && first + i == weight.last && kg >= 2) {   // past K
 #pragma unroll
         for (int j = 0; j < TN; ++j) w[j] = v4u{0, 0, 0, 0};
 #pragma unroll
@@ -371,14 +397,12 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
 // A workgroup owns a BM x 256 tile of one expert's outputs: four waves, each all BM = 32 TM rows of
 // x and 64 of the weight's rows (TM x 2 products of 32x32x16). K advances in steps of 64.
 //
-// A wave needs its weight rows for itself alone, so the codes go from global memory to registers
-// and are decoded there: lane l holds row l % 32 and, as one 16-byte load, the 32 codes of K half
-// l / 32, which feed four products (the order of k inside a step is free as long as both operands
-// agree). The rows of x, which every wave needs, go straight from global memory into LDS, double
-// buffered. Per step of a 256 x 256 tile the LDS serves 128 KiB of reads and 32 KiB of writes (1280
-// cycles at 128 bytes a cycle) against 2048 cycles of matrix products; staging the decoded weights
-// in LDS as well, with 128 x 64 outputs to a wave, took 256 KiB (2048 cycles), and was the slower
-// by the figures below.
+// A wave needs its weight rows for itself alone, so it copies their codes and scales a turn of 128 k
+// at a time and decodes them in registers: lane l holds row l % 32 and the 32 codes of K half l / 32
+// of a step, which feed four products (the order of k inside a step is free as long as both operands
+// agree). The rows of x, which every wave needs, are copied into LDS a step at a time, NXB steps
+// deep. Staging the decoded weight in LDS instead, with 128 x 64 outputs to a wave, was slower: 1.24
+// ms against 0.96 for 8192 rows of eight experts, 4096 -> 14336.
 //
 // Fragments are read one product group ahead. The barrier of a step stands before its last group:
 // by then the step's own reads are done and the next step's rows have landed, so the next buffer's
@@ -447,12 +471,27 @@ struct TileArgs {
 };
 
 // E8: power-of-two scales (block 32), else 3-mantissa-bit ones with block B. PLANES: bf16 parts of x.
-template <bool E8, int B, int PLANES, int TM, int TILE_NW>
-__global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void k_wlinear_tile(WParams p, TileArgs t) {
-  constexpr int BM = TM * 32, STAGE = BM * ROWB, TN = TILE_BN / 32 / TILE_NW, PIECES = BM / 8 / TILE_NW;
-  constexpr int OW = TN * 32, OLD = OW + 4;   // a wave's output columns, padded by 16 bytes
-  constexpr int OUTB = TILE_NW * 32 * OLD * 4;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE > OUTB ? 2 * STAGE : OUTB];
+template <bool E8_, int B_, int PLANES_, int TM_, bool BYTES_>
+struct TileForm {
+  static constexpr bool E8 = E8_;
+  static constexpr int B = B_, PLANES = PLANES_, TM = TM_;
+  // eight waves of 256 x 32 outputs for the tallest tile, else four of 32 TM x 64
+  static constexpr int NW = TM == 8 ? 8 : 4, TN = TILE_BN / 32 / NW;
+  static constexpr int BM = TM * 32, STAGE = BM * ROWB, PIECES = BM / 8 / NW;
+  static constexpr int NXB = TM == 3 || TM == 4 ? 2 : 3;   // three leave no second workgroup its LDS there
+  using Weight = WeightTurns<B, BYTES_, TN * 2>;
+  static constexpr int WBYTES = 2 * Weight::SIZE;          // a wave's two turns
+  static constexpr int OW = TN * 32, OLD = OW + 4;         // a wave's output columns, padded by 16 bytes
+  static constexpr int LDS = NXB * STAGE + NW * WBYTES;
+  static_assert(NW * 32 * OLD * 4 <= LDS, "the output rows fit the buffers");
+};
+
+template <class F>
+__global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileArgs t) {
+  constexpr bool E8 = F::E8;
+  constexpr int B = F::B, PLANES = F::PLANES, TM = F::TM, TN = F::TN, TILE_NW = F::NW, BM = F::BM, STAGE = F::STAGE;
+  constexpr int PIECES = F::PIECES, OW = F::OW, OLD = F::OLD, NXB = F::NXB;
+  __shared__ __attribute__((aligned(1024))) char lds[F::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   TileMap<BM> map;
   const uint32_t mtiles = p.offsets ? map.count(p) : t.mtiles;
@@ -491,8 +530,10 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
     const int rc = (int)min((int64_t)r, m1 - 1 - m0);
     xoff[j] = (uint32_t)(rc * p.ldx * 2) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
   }
-  const int ksteps = (int)(p.K / BK);
-  const int k0 = (int)((int64_t)ksteps * slice / t.slices), k1 = (int)((int64_t)ksteps * (slice + 1) / t.slices);
+  // this slice's steps of K, whole turns (two steps) but for the last
+  const int ksteps = (int)(p.K / BK), turns = (ksteps + 1) / 2;
+  const int turn0 = (int)((int64_t)turns * slice / t.slices), turn1 = (int)((int64_t)turns * (slice + 1) / t.slices);
+  const int k0 = turn0 * 2, k1 = min(turn1 * 2, ksteps);
   const char* xsrc = uniform_ptr(p.x + m0 * p.ldx * 2 + (int64_t)k0 * ROWB);   // the next rows to copy
   const int steps = (k1 - k0) * PLANES;
   int xplane = 0;
@@ -508,52 +549,24 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
     }
   };
 
-  // weight: this lane's rows
+  // weight: this wave's rows (waves past the weight's last row take its last rows; not stored)
   const int fr = lane & 31, fk = lane >> 5;
-  constexpr int NS = E8 || B == 32 ? 1 : 2;   // scale codes of 32 codes
-  const uint8_t* qp[TN];
-  const uint8_t* sp[TN];
-#pragma unroll
-  for (int i = 0; i < TN; ++i) {
-    const int64_t n = min(n0 + wave * OW + i * 32 + fr, p.N - 1);
-    qp[i] = p.q + ((int64_t)e * p.N + n) * (p.K / 2) + (int64_t)k0 * (BK / 2) + fk * 16;
-    sp[i] = p.s + (int64_t)e * p.s_stride + (n >> t.f.s_band) * t.f.s_row + ((int64_t)k0 * 2 + fk) * NS * t.f.s_k;
-  }
-  v4u codes[TN], cnext[TN];
-  uint32_t sc[TN][NS], snext[TN][NS];
-  int kload = k0;
-  auto load_codes = [&] {   // the step kload; past the slice's last step that step again (not used), without a branch
-    const int64_t on = kload + 1 < k1 ? 1 : 0;
-    ++kload;
+  typename F::Weight weight;
+  weight.init(p, t.f, e, min(n0 + wave * OW, (p.N - 1) & ~(int64_t)15));
+  char* wring = lds + NXB * STAGE + wave * F::WBYTES;
+  v4u codes[TN];
+  uint32_t sc[TN][2];
+  auto take_codes = [&](int k) {   // the codes of step k, whose turn has landed
+    const char* turn = wring + ((k >> 1) & 1) * F::Weight::SIZE;
+    const int piece = (k & 1) * 2 + fk;
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
-      cnext[i] = *reinterpret_cast<const v4u*>(qp[i]);
-      qp[i] += on * (BK / 2);
-#pragma unroll
-      for (int h = 0; h < NS; ++h) snext[i][h] = sp[i][h * t.f.s_k];
-      sp[i] += on * 2 * NS * t.f.s_k;
-    }
-  };
-  // The codes have landed (after wait_copies()): without this the compiler, which does not see that
-  // wait, waits at their first use for every copy issued since.
-  auto pin_codes = [&] {
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      pin(cnext[i]);
-#pragma unroll
-      for (int h = 0; h < NS; ++h) pin(snext[i][h]);
-    }
-  };
-  auto take_codes = [&] {
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      codes[i] = cnext[i];
-#pragma unroll
-      for (int h = 0; h < NS; ++h) sc[i][h] = snext[i][h];
+      codes[i] = F::Weight::codes(turn, i * 32 + fr, piece);
+      F::Weight::scales(turn, i * 32 + fr, piece, sc[i]);
     }
   };
   auto decode = [&](int i, int s) {   // dword s: k = 32 (lane / 32) + 8 s ..
-    const float sv = code_value<E8>(sc[i][s * NS / 4], t.f.scale_mul);
+    const float sv = code_value<E8>(sc[i][s / 2], t.f.scale_mul);
     return decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(codes[i][s], sv);
   };
 
@@ -565,42 +578,48 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  char* buf = lds;
-  char* nxt = lds + STAGE;
-  copy_x(buf);
-  if (steps > 1) copy_x(nxt);
-  load_codes();
-  take_codes();
-  load_codes();
+  weight.copy(turn0, wring + (turn0 & 1) * F::Weight::SIZE);
+  if (turn0 + 1 < turn1) weight.copy(turn0 + 1, wring + ((turn0 + 1) & 1) * F::Weight::SIZE);
+  char* xbuf[NXB];   // of this step, the next ..
+#pragma unroll
+  for (int i = 0; i < NXB; ++i) {
+    xbuf[i] = lds + i * STAGE;
+    if (i < steps) copy_x(xbuf[i]);
+  }
+  wait_copies();
+  __syncthreads();
   v8bf bw[TN][4];   // the decoded weight of a step, dword by dword
+  take_codes(k0);
 #pragma unroll
   for (int s = 0; s < 3; ++s)
 #pragma unroll
     for (int i = 0; i < TN; ++i) bw[i][s] = decode(i, s);
-  wait_copies();
-  pin_codes();
-  __syncthreads();
   v8bf ax[2][TM];
   auto read_x = [&](const char* from, int s, v8bf* to) {
 #pragma unroll
     for (int j = 0; j < TM; ++j) to[j] = *reinterpret_cast<const v8bf*>(from + swz(j * 32 + fr, fk * 4 + s));
   };
-  read_x(buf, 0, ax[0]);
-  int plane = 0;
+  read_x(xbuf[0], 0, ax[0]);
+  int plane = 0, k = k0;
   for (int st = 0; st < steps; ++st) {
     const bool first = PLANES == 1 || plane == 0, last = PLANES == 1 || plane == PLANES - 1;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s == 3) {
-        // (past the last step: an unused read of the other buffer, so that no path joins here with
-        // this step's fragments still being waited for)
-        wait_copies();
-        pin_codes();
+        // The next step's rows have landed and this wave's reads of this step's are done. The newest
+        // copies are of rows (a step's codes are copied before its rows), so the codes have, too.
+        if (NXB == 3 && st + 2 < steps) wait_all_but<PIECES>();
+        else wait_all_but<0>();
+        wait_lds();
         __syncthreads();
-        if (st + 2 < steps) copy_x(buf);
-        read_x(nxt, 0, ax[0]);
+        // the turn whose last codes this step took, and this step's rows, make room
+        if (last && (k & 1) == 0 && (k >> 1) + 2 < turn1) weight.copy((k >> 1) + 2, wring + ((k >> 1) & 1) * F::Weight::SIZE);
+        if (st + NXB < steps) copy_x(xbuf[0]);
+        // (past the last step: an unused read of another buffer, so that no path joins here with
+        // this step's fragments still being waited for)
+        read_x(xbuf[1], 0, ax[0]);
       } else {
-        read_x(buf, s + 1, ax[(s + 1) & 1]);
+        read_x(xbuf[0], s + 1, ax[(s + 1) & 1]);
       }
 #pragma unroll
       for (int j = 0; j < TM; ++j)
@@ -613,10 +632,7 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
 #pragma unroll
         for (int i = 0; i < TN; ++i) bw[i][(s + 3) & 3] = decode(i, (s + 3) & 3);
       }
-      if (s == 0 && last) {
-        take_codes();
-        load_codes();
-      }
+      if (s == 0 && last) take_codes(k + 1);   // (past the last step: unused bytes of the ring)
       // per TN products one fragment read and a share of the decoding
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
@@ -624,12 +640,13 @@ __global__ __launch_bounds__(TILE_NW * 64, TM >= 8 && TILE_NW == 4 ? 1 : 2) void
         __builtin_amdgcn_sched_group_barrier(0x008, TN, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, ((E8 ? 6 : 19) * TN + TM - 1) / TM, 0);
       }
-      if (s == 0) __builtin_amdgcn_sched_group_barrier(0x020, TN * (1 + NS), 0);   // the next step's codes
     }
     if (PLANES > 1) plane = last ? 0 : plane + 1;
-    char* const b = buf;
-    buf = nxt;
-    nxt = b;
+    if (last) ++k;
+    char* const b = xbuf[0];
+#pragma unroll
+    for (int i = 0; i + 1 < NXB; ++i) xbuf[i] = xbuf[i + 1];
+    xbuf[NXB - 1] = b;
   }
 
   // Out: lane l of a product holds row m = l % 32 and columns n = 8 (r / 4) + 4 (l / 32) + r % 4.
@@ -724,7 +741,7 @@ TilePlan plan_tiles(const WLinearArgs& a) {
   const int64_t cus = device_cu_count(), groups = a.offsets_given ? a.n_experts : 0, ksteps = a.K / BK;
   TilePlan best{};
   double least = 0;
-  for (int tm : {8, 4, 2, 1}) {
+  for (int tm : {8, 4, 3, 2, 1}) {
     TilePlan t;
     t.tm = tm;
     t.nt = div_up(a.N, TILE_BN);
@@ -745,19 +762,19 @@ size_t planes_bytes(const WLinearArgs& a) { return a.x_f32 ? (size_t)div_up(3 * 
 
 template <bool E8, int B, int PLANES>
 void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
+  using std::integral_constant;
+  // scale codes byte by byte where a turn's are not aligned words
+  const bool bytes = f.s_k != 1 || (B == 32 && a.K % TURN_K != 0);
   if (!use_tile(a)) {
     const uint32_t groups = a.offsets ? a.n_experts + 1 : 1;
     // as many products to an activation fragment as leave no compute unit without a workgroup
     const int64_t cus = device_cu_count(), each = a.n_experts;
     const int tn = PLANES == 1 && div_up(a.N, 64) * each >= cus ? 4 : div_up(a.N, 32) * each >= cus ? 2 : 1;
-    // scale codes byte by byte where a turn's are not aligned words
-    const bool bytes = f.s_k != 1 || (B == 32 && a.K % ROWS_K != 0);
     auto go = [&](auto tn_, auto xr_, auto bytes_) {
       using F = RowsForm<E8, B, PLANES, decltype(tn_)::value, decltype(xr_)::value, decltype(bytes_)::value>;
       const dim3 grid((uint32_t)div_up(a.N, 16 * F::TN), groups);
       k_wlinear_rows<F><<<grid, F::NW * 64, 0, a.stream>>>(p, f);
     };
-    using std::integral_constant;
     auto with_bytes = [&](auto tn_, auto xr_) { bytes ? go(tn_, xr_, std::true_type{}) : go(tn_, xr_, std::false_type{}); };
     // Activation rows at a time. An expert with more rows than that reads its weight again (from the
     // caches); rows that are not there cost copies and LDS: 16 slots over 8 experts took 73 us with
@@ -789,10 +806,21 @@ void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
     t.f.y_vec = a.N % 4 == 0;
   }
   const uint32_t grid = (uint32_t)(div_up(plan.mt * plan.nt * plan.slices, 8) * 8);
-  if (plan.tm == 1) k_wlinear_tile<E8, B, PLANES, 1, 4><<<grid, 256, 0, a.stream>>>(p, t);
-  else if (plan.tm == 2) k_wlinear_tile<E8, B, PLANES, 2, 4><<<grid, 256, 0, a.stream>>>(p, t);
-  else if (plan.tm == 4) k_wlinear_tile<E8, B, PLANES, 4, 4><<<grid, 256, 0, a.stream>>>(p, t);
-  else k_wlinear_tile<E8, B, PLANES, 8, 8><<<grid, 512, 0, a.stream>>>(p, t);
+  auto go = [&](auto tm_) {
+    constexpr int TM = decltype(tm_)::value;
+    if (bytes) {
+      using F = TileForm<E8, B, PLANES, TM, true>;
+      k_wlinear_tile<F><<<grid, F::NW * 64, 0, a.stream>>>(p, t);
+    } else {
+      using F = TileForm<E8, B, PLANES, TM, false>;
+      k_wlinear_tile<F><<<grid, F::NW * 64, 0, a.stream>>>(p, t);
+    }
+  };
+  if (plan.tm == 1) go(integral_constant<int, 1>{});
+  else if (plan.tm == 2) go(integral_constant<int, 2>{});
+  else if (plan.tm == 3) go(integral_constant<int, 3>{});
+  else if (plan.tm == 4) go(integral_constant<int, 4>{});
+  else go(integral_constant<int, 8>{});
   if (t.part) {
     const uint32_t join = (uint32_t)std::min<int64_t>(div_up(a.rows * a.N, 256), 4096);
     if (a.y_f32) k_join_slices<true><<<join, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
