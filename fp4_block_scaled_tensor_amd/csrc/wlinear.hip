@@ -478,7 +478,7 @@ struct TileForm {
   // eight waves of 256 x 32 outputs for the tallest tile, else four of 32 TM x 64
   static constexpr int NW = TM == 8 ? 8 : 4, TN = TILE_BN / 32 / NW;
   static constexpr int BM = TM * 32, STAGE = BM * ROWB, PIECES = BM / 8 / NW;
-  static constexpr int NXB = TM == 3 || TM == 4 ? 2 : 3;   // three leave no second workgroup its LDS there
+  static constexpr int NXB = TM == 8 ? 3 : 2;              // three would take the second workgroup's LDS below 8
   using Weight = WeightTurns<B, BYTES_, TN * 2>;
   static constexpr int WBYTES = 2 * Weight::SIZE;          // a wave's two turns
   static constexpr int OW = TN * 32, OLD = OW + 4;         // a wave's output columns, padded by 16 bytes
@@ -580,7 +580,7 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
 
   weight.copy(turn0, wring + (turn0 & 1) * F::Weight::SIZE);
   if (turn0 + 1 < turn1) weight.copy(turn0 + 1, wring + ((turn0 + 1) & 1) * F::Weight::SIZE);
-  char* xbuf[NXB];   // of this step, the next ..
+  char* xbuf[NXB];   // the rows of this step, the next ..
 #pragma unroll
   for (int i = 0; i < NXB; ++i) {
     xbuf[i] = lds + i * STAGE;
@@ -606,17 +606,14 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s == 3) {
-        // The next step's rows have landed and this wave's reads of this step's are done. The newest
-        // copies are of rows (a step's codes are copied before its rows), so the codes have, too.
+        // The next step's rows have landed, and this wave's reads of this step's are done. The newest
+        // copies are of rows (codes are copied before the rows of a step), so the codes have, too.
+        // (Past the last step: an unused read of another buffer, so that no path joins here with this
+        // step's fragments still being waited for.)
         if (NXB == 3 && st + 2 < steps) wait_all_but<PIECES>();
         else wait_all_but<0>();
         wait_lds();
         __syncthreads();
-        // the turn whose last codes this step took, and this step's rows, make room
-        if (last && (k & 1) == 0 && (k >> 1) + 2 < turn1) weight.copy((k >> 1) + 2, wring + ((k >> 1) & 1) * F::Weight::SIZE);
-        if (st + NXB < steps) copy_x(xbuf[0]);
-        // (past the last step: an unused read of another buffer, so that no path joins here with
-        // this step's fragments still being waited for)
         read_x(xbuf[1], 0, ax[0]);
       } else {
         read_x(xbuf[0], s + 1, ax[(s + 1) & 1]);
@@ -626,6 +623,13 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
 #pragma unroll
         for (int i = 0; i < TN; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw[i][s], ax[s & 1][j], acc[i][j], 0, 0, 0);
+      if (s == 3) {
+        // The turn whose last codes this step took, and this step's rows, make room. Behind the
+        // group's products: issued before them, the copies left the matrix cores idle (801 us
+        // against 740 for 8192 x 4096 -> 14336).
+        if (last && (k & 1) == 0 && (k >> 1) + 2 < turn1) weight.copy((k >> 1) + 2, wring + ((k >> 1) & 1) * F::Weight::SIZE);
+        if (st + NXB < steps) copy_x(xbuf[0]);
+      }
       // group 0 decodes this step's last dword; groups 1 to 3 replace dwords 0 to 2, whose products
       // are under way, by the next step's
       if (s == 0 ? first : last) {
@@ -736,7 +740,8 @@ struct TilePlan {
 // The tile height with the least rounds of tiles over the compute units times the time of a tile,
 // which is about that of its products and one more. Measured, 8192 rows 4096 -> 14336: 113, 61 and
 // 42 us a round for tm 8, 4 and 2; 2048 rows 4096 -> 6144: 118 us at 8 (192 tiles), 139 at 4 (384).
-// A K long enough is split where the tiles alone leave compute units idle.
+// A K long enough is split where the tiles alone leave compute units idle; the
+// low tiles, which are bound by latency, into two workgroups to a unit (24 rows 4096 -> 28672: 37 us, 45 with one).
 TilePlan plan_tiles(const WLinearArgs& a) {
   const int64_t cus = device_cu_count(), groups = a.offsets_given ? a.n_experts : 0, ksteps = a.K / BK;
   TilePlan best{};
@@ -747,7 +752,7 @@ TilePlan plan_tiles(const WLinearArgs& a) {
     t.nt = div_up(a.N, TILE_BN);
     t.mt = div_up(a.rows, tm * 32) + groups;
     const int64_t tiles = (div_up(a.rows, tm * 32) + groups / 2) * t.nt;   // an expert's last tile is half full
-    t.slices = (int)std::max<int64_t>(1, std::min<int64_t>(cus / tiles, ksteps / 4));
+    t.slices = (int)std::max<int64_t>(1, std::min<int64_t>((tm <= 2 ? 2 : 1) * cus / tiles, ksteps / 4));
     const double cost = (double)div_up(tiles * t.slices, cus) * (tm + 1) / t.slices;
     if (best.tm == 0 || cost < least) {
       best = t;
