@@ -13,9 +13,11 @@ namespace {
 // slot order and no atomic decides an order. Keys are the expert ids; a dropped slot has key E.
 constexpr int SORT_ONE_WAVES = 16;       // the one-workgroup form
 constexpr int SORT_ONE_MAX = 8192;       // slots it takes
-constexpr int SORT_WAVES = 8;            // the form with one workgroup per chunk
-constexpr int SORT_CHUNK = 2048;         // slots per chunk
 constexpr int SORT_ONE_EXPERTS = 512;    // experts it takes (16 LDS rows of E + 1 counters below 64 KiB)
+constexpr int SORT_WAVE_SLOTS = 256;     // slots of a wave in the form with one workgroup per chunk
+// waves of that form: every workgroup sums its columns of the chunks' counts, so fewer, larger chunks
+// are better (262144 slots, 128 experts: 13.6 us with 128 chunks of 8 waves)
+constexpr int sort_waves(int E) { return E <= SORT_ONE_EXPERTS ? 16 : 8; }
 
 template <bool ID64>
 __device__ __forceinline__ uint32_t slot_key(const void* ids, int64_t ld, int topk, int64_t slot, int E) {
@@ -144,14 +146,15 @@ __global__ __launch_bounds__(SORT_ONE_WAVES * 64) void k_sort_one(const void* __
 }
 
 // counts[chunk][E + 1]
-template <bool ID64>
+template <bool ID64, int SORT_WAVES>
 __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_count(const void* __restrict__ ids, int64_t ld, int topk,
                                                                 int n, int E, int32_t* __restrict__ counts) {
   extern __shared__ int rows[];   // [E + 1]
   const int keys = E + 1;
   for (int i = threadIdx.x; i < keys; i += SORT_WAVES * 64) rows[i] = 0;
   __syncthreads();
-  const int64_t lo = (int64_t)blockIdx.x * SORT_CHUNK, hi = min((int64_t)n, lo + SORT_CHUNK);
+  constexpr int CHUNK = SORT_WAVES * SORT_WAVE_SLOTS;
+  const int64_t lo = (int64_t)blockIdx.x * CHUNK, hi = min((int64_t)n, lo + CHUNK);
   for (int64_t s = lo + threadIdx.x; s < hi; s += SORT_WAVES * 64)
     atomicAdd(&rows[slot_key<ID64>(ids, ld, topk, s, E)], 1);
   __syncthreads();
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_count(const void* __re
 
 // Each workgroup sums the counts of all chunks (its keys' totals) and of the chunks before its
 // own, scans the totals into the experts' offsets and places its chunk.
-template <bool ID64>
+template <bool ID64, int SORT_WAVES>
 __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_place(const void* __restrict__ ids, int64_t ld, int topk,
                                                                 int n, int E, int bits,
                                                                 const int32_t* __restrict__ counts,
@@ -175,9 +178,8 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_place(const void* __re
   int* rows = lds + 2 * keys;
   for (int i = threadIdx.x; i < (2 + SORT_WAVES) * keys; i += NTH) lds[i] = 0;
   __syncthreads();
-  constexpr int SEG = SORT_CHUNK / SORT_WAVES;
-  const int64_t c0 = (int64_t)chunk * SORT_CHUNK;
-  const int64_t lo = min((int64_t)n, c0 + w * SEG), hi = min((int64_t)n, lo + SEG);
+  const int64_t lo = min((int64_t)n, ((int64_t)chunk * SORT_WAVES + w) * SORT_WAVE_SLOTS);
+  const int64_t hi = min((int64_t)n, lo + SORT_WAVE_SLOTS);
   wave_count<ID64>(ids, ld, topk, E, lo, hi, rows + w * keys);
   // the keys' columns of counts, `parts` threads to a key when there are few keys
   const int parts = keys >= NTH ? 1 : NTH / keys;
@@ -228,15 +230,25 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_place(const void* __re
 // ---------------------------------------------------------------- rows to and from expert order
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-// V consecutive elements of a row as float32: 16 bytes (V = 8 bf16 or 4 float32) or one element.
-template <bool F32, bool VEC>
+// Up to V consecutive elements of a row as float32: 16 bytes (8 bf16 or 4 float32). Rows that are
+// not 16-byte aligned take the same 16-byte accesses at the alignment of their elements (the memory
+// path allows that) and end in single elements.
+template <bool F32, bool ALIGNED>
 struct Elems {
-  static constexpr int V = VEC ? (F32 ? 4 : 8) : 1;
-  static constexpr int ESZ = F32 ? 4 : 2;
-  static __device__ __forceinline__ v4u raw(const char* p) { return *reinterpret_cast<const v4u*>(p); }
-  static __device__ __forceinline__ void load(const char* p, float* v) {
-    if constexpr (VEC) {
-      const v4u r = raw(p);
+  static constexpr int V = F32 ? 4 : 8, ESZ = F32 ? 4 : 2;
+  static __device__ __forceinline__ float get(const char* p) {
+    if constexpr (F32) return *reinterpret_cast<const float*>(p);
+    else return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+  }
+  static __device__ __forceinline__ void put(char* p, float v) {
+    if constexpr (F32) *reinterpret_cast<float*>(p) = v;
+    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack_bf16(v, 0.0f);
+  }
+  // n elements are there; the others are zero
+  static __device__ __forceinline__ void load(const char* p, int64_t n, float* v) {
+    if (ALIGNED || n >= V) {
+      v4u r;
+      __builtin_memcpy(&r, ALIGNED ? __builtin_assume_aligned(p, 16) : __builtin_assume_aligned(p, ESZ), 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (F32) {
@@ -246,73 +258,63 @@ struct Elems {
           v[2 * i + 1] = bf16_hi(r[i]);
         }
       }
-    } else if constexpr (F32) {
-      v[0] = *reinterpret_cast<const float*>(p);
     } else {
-      v[0] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = i < n ? get(p + i * ESZ) : 0.0f;
     }
   }
-  static __device__ __forceinline__ void store(char* p, const float* v) {
-    if constexpr (VEC) {
+  static __device__ __forceinline__ void store(char* p, int64_t n, const float* v) {
+    if (ALIGNED || n >= V) {
       v4u r;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (F32) r[i] = __float_as_uint(v[i]);
         else r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
       }
-      *reinterpret_cast<v4u*>(p) = r;
-    } else if constexpr (F32) {
-      *reinterpret_cast<float*>(p) = v[0];
+      __builtin_memcpy(ALIGNED ? __builtin_assume_aligned(p, 16) : __builtin_assume_aligned(p, ESZ), &r, 16);
     } else {
-      *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack_bf16(v[0], 0.0f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) put(p + i * ESZ, v[i]);
     }
   }
 };
 
 constexpr int MT = 256;   // threads of the row kernels
 
-// One token's row to its slots' rows: a plain copy (gather), or w[s] times it (gradient of the
-// combined rows).
-template <bool F32, bool VEC, bool WEIGHT>
+// One token's row to its slots' rows (gather): the row is read once and written topk times.
+template <bool F32, bool ALIGNED>
 __global__ __launch_bounds__(MT) void k_spread(const char* __restrict__ x, int64_t ldx, int64_t hidden,
                                                const int32_t* __restrict__ pos, int topk, int64_t n,
-                                               const float* __restrict__ w, int64_t ldw, char* __restrict__ xs,
-                                               int64_t ldxs) {
-  using E = Elems<F32, VEC>;
+                                               char* __restrict__ xs, int64_t ldxs) {
+  using E = Elems<F32, ALIGNED>;
   const int64_t t = blockIdx.x;
   for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
-    float v[E::V];
-    E::load(x + (t * ldx + h) * E::ESZ, v);
+    float v[E::V], zero[E::V] = {};
+    E::load(x + (t * ldx + h) * E::ESZ, hidden - h, v);
     for (int j = 0; j < topk; ++j) {
       const int32_t p = pos[t * topk + j];
       const int64_t row = p < 0 ? ~p : p;
-      if (row >= n) continue;
-      float o[E::V];
-      const float f = WEIGHT && p >= 0 ? w[t * ldw + j] : 1.0f;
-#pragma unroll
-      for (int i = 0; i < E::V; ++i) o[i] = p < 0 ? 0.0f : (WEIGHT ? f * v[i] : v[i]);
-      E::store(xs + (row * ldxs + h) * E::ESZ, o);
+      if (row < n) E::store(xs + (row * ldxs + h) * E::ESZ, hidden - h, p < 0 ? zero : v);
     }
   }
 }
 
 // A token's slots' rows summed, with weights or without.
-template <bool F32, bool VEC, bool WEIGHT>
+template <bool F32, bool ALIGNED, bool WEIGHT>
 __global__ __launch_bounds__(MT) void k_join(const char* __restrict__ ys, int64_t ldys, int64_t hidden,
                                              const int32_t* __restrict__ pos, int topk, int64_t n,
                                              const float* __restrict__ w, int64_t ldw, char* __restrict__ y,
                                              int64_t ldy) {
-  using E = Elems<F32, VEC>;
+  using E = Elems<F32, ALIGNED>;
   const int64_t t = blockIdx.x;
   for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
-    float a[E::V];
-#pragma unroll
-    for (int i = 0; i < E::V; ++i) a[i] = 0.0f;
+    float a[E::V] = {};
     for (int j = 0; j < topk; ++j) {
       const int32_t p = pos[t * topk + j];
       if (p < 0 || p >= n) continue;
       float v[E::V];
-      E::load(ys + ((int64_t)p * ldys + h) * E::ESZ, v);
+      E::load(ys + ((int64_t)p * ldys + h) * E::ESZ, hidden - h, v);
       if constexpr (WEIGHT) {
         const float f = w[t * ldw + j];
 #pragma unroll
@@ -322,35 +324,77 @@ __global__ __launch_bounds__(MT) void k_join(const char* __restrict__ ys, int64_
         for (int i = 0; i < E::V; ++i) a[i] += v[i];
       }
     }
-    E::store(y + (t * ldy + h) * E::ESZ, a);
+    E::store(y + (t * ldy + h) * E::ESZ, hidden - h, a);
   }
 }
 
-// dw[s] = <dy[s / topk], ys[pos[s]]>: a workgroup per slot.
-template <bool F32, bool VEC>
-__global__ __launch_bounds__(MT) void k_slot_dot(const char* __restrict__ dy, int64_t lddy,
-                                                 const char* __restrict__ ys, int64_t ldys, int64_t hidden,
-                                                 const int32_t* __restrict__ pos, int topk, int64_t n,
-                                                 float* __restrict__ dw, int64_t lddw) {
-  using E = Elems<F32, VEC>;
-  __shared__ float part[MT / 64];
-  const int64_t s = blockIdx.x, t = s / topk;
-  const int32_t p = pos[s];
-  float a = 0.0f;
-  if (p >= 0 && p < n) {
-    for (int64_t h = (int64_t)threadIdx.x * E::V; h < hidden; h += MT * E::V) {
-      float u[E::V], v[E::V];
-      E::load(dy + (t * lddy + h) * E::ESZ, u);
-      E::load(ys + ((int64_t)p * ldys + h) * E::ESZ, v);
+// Gradient of the weighted sum: a workgroup takes a token's dy, scales it into its slots' rows of
+// dys and multiplies it with their rows of ys for dw. dy is read once: R chunks of it stay in
+// registers (longer rows read the rest again, from the caches).
+constexpr int JB = 64;   // slots whose partial sums are kept at a time
+template <bool F32, bool ALIGNED, int R>
+__global__ __launch_bounds__(MT) void k_combine_grad(const char* __restrict__ dy, int64_t lddy,
+                                                     const char* __restrict__ ys, int64_t ldys, int64_t hidden,
+                                                     const float* __restrict__ w, int64_t ldw,
+                                                     const int32_t* __restrict__ pos, int topk, int64_t n,
+                                                     char* __restrict__ dys, int64_t lddys, float* __restrict__ dw,
+                                                     int64_t lddw) {
+  using E = Elems<F32, ALIGNED>;
+  constexpr int STEP = MT * E::V;
+  __shared__ float part[JB][MT / 64];
+  const int64_t t = blockIdx.x, h0 = (int64_t)threadIdx.x * E::V;
+  float u[R][E::V];
 #pragma unroll
-      for (int i = 0; i < E::V; ++i) a = __builtin_fmaf(u[i], v[i], a);
+  for (int c = 0; c < R; ++c) {
+    const int64_t h = h0 + c * STEP;
+    if (h < hidden) {
+      E::load(dy + (t * lddy + h) * E::ESZ, hidden - h, u[c]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E::V; ++i) u[c][i] = 0.0f;
     }
   }
+  for (int j0 = 0; j0 < topk; j0 += JB) {
+    const int jn = min(JB, topk - j0);
+    for (int j = 0; j < jn; ++j) {
+      const int32_t p = pos[t * topk + j0 + j];
+      const int64_t row = p < 0 ? ~p : p;
+      const bool kept = p >= 0 && row < n;
+      float a = 0.0f;
+      if (row < n) {
+        const float f = kept && dys ? w[t * ldw + j0 + j] : 0.0f;
+        auto chunk = [&](int64_t h, const float* g) {
+          if (dys) {
+            float o[E::V];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) a += __shfl_xor(a, o, 64);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = a;
-  __syncthreads();
-  if (threadIdx.x == 0) dw[t * lddw + (s - t * topk)] = (part[0] + part[1]) + (part[2] + part[3]);
+            for (int i = 0; i < E::V; ++i) o[i] = kept ? f * g[i] : 0.0f;
+            E::store(dys + (row * lddys + h) * E::ESZ, hidden - h, o);
+          }
+          if (kept && dw) {
+            float v[E::V];
+            E::load(ys + (row * ldys + h) * E::ESZ, hidden - h, v);
+#pragma unroll
+            for (int i = 0; i < E::V; ++i) a = __builtin_fmaf(g[i], v[i], a);
+          }
+        };
+#pragma unroll
+        for (int c = 0; c < R; ++c)
+          if (h0 + c * STEP < hidden) chunk(h0 + c * STEP, u[c]);
+        for (int64_t h = h0 + R * STEP; h < hidden; h += STEP) {
+          float g[E::V];
+          E::load(dy + (t * lddy + h) * E::ESZ, hidden - h, g);
+          chunk(h, g);
+        }
+      }
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) a += __shfl_xor(a, o, 64);
+      if ((threadIdx.x & 63) == 0) part[j][threadIdx.x >> 6] = a;
+    }
+    __syncthreads();
+    if (dw && threadIdx.x < jn)
+      dw[t * lddw + j0 + threadIdx.x] = (part[threadIdx.x][0] + part[threadIdx.x][1]) + (part[threadIdx.x][2] + part[threadIdx.x][3]);
+    __syncthreads();
+  }
 }
 
 bool vec_ok(const void* p, int64_t ld, int64_t esz) {
@@ -359,16 +403,15 @@ bool vec_ok(const void* p, int64_t ld, int64_t esz) {
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// f(F32, VEC) with both as compile-time constants
+// f(F32, ALIGNED) with both as compile-time constants
 template <class F>
 void by_type(bool f32, bool vec, F&& f) {
   if (f32) vec ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
   else vec ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
 }
 
-dim3 row_grid(const RowsArgs& a, bool vec) {
-  const int64_t v = vec ? (a.f32 ? 4 : 8) : 1;
-  return dim3((uint32_t)a.tokens, (uint32_t)std::min<int64_t>(div_up(a.hidden, MT * v), 1024));
+dim3 row_grid(const RowsArgs& a) {
+  return dim3((uint32_t)a.tokens, (uint32_t)std::min<int64_t>(div_up(a.hidden, MT * (a.f32 ? 4 : 8)), 1024));
 }
 
 bool sort_in_one(int64_t n, int E) { return n <= SORT_ONE_MAX && E <= SORT_ONE_EXPERTS; }
@@ -376,7 +419,7 @@ bool sort_in_one(int64_t n, int E) { return n <= SORT_ONE_MAX && E <= SORT_ONE_E
 }  // namespace
 
 size_t expert_sort_ws(int64_t n, int E) {
-  return sort_in_one(n, E) ? 0 : (size_t)div_up(n, SORT_CHUNK) * (size_t)(E + 1) * sizeof(int32_t);
+  return sort_in_one(n, E) ? 0 : (size_t)div_up(n, sort_waves(E) * SORT_WAVE_SLOTS) * (size_t)(E + 1) * sizeof(int32_t);
 }
 
 hipError_t run_expert_sort(const SortArgs& a) {
@@ -390,12 +433,15 @@ hipError_t run_expert_sort(const SortArgs& a) {
           a.ids, a.ld_ids, a.topk, n, E, bits, a.order, a.pos, a.offsets);
       return;
     }
-    const uint32_t chunks = (uint32_t)div_up(n, SORT_CHUNK);
     int32_t* counts = reinterpret_cast<int32_t*>(a.ws);
-    k_sort_count<ID64><<<chunks, SORT_WAVES * 64, (E + 1) * sizeof(int), a.stream>>>(a.ids, a.ld_ids, a.topk, n, E,
-                                                                                    counts);
-    k_sort_place<ID64><<<chunks, SORT_WAVES * 64, (2 + SORT_WAVES) * (E + 1) * sizeof(int), a.stream>>>(
-        a.ids, a.ld_ids, a.topk, n, E, bits, counts, a.order, a.pos, a.offsets);
+    auto chunked = [&](auto waves) {
+      constexpr int W = decltype(waves)::value;
+      const uint32_t chunks = (uint32_t)div_up(n, W * SORT_WAVE_SLOTS);
+      k_sort_count<ID64, W><<<chunks, W * 64, (E + 1) * sizeof(int), a.stream>>>(a.ids, a.ld_ids, a.topk, n, E, counts);
+      k_sort_place<ID64, W><<<chunks, W * 64, (2 + W) * (E + 1) * sizeof(int), a.stream>>>(a.ids, a.ld_ids, a.topk, n, E, bits, counts, a.order, a.pos, a.offsets);
+    };
+    if (sort_waves(E) == 16) chunked(std::integral_constant<int, 16>{});
+    else chunked(std::integral_constant<int, 8>{});
   };
   if (a.id64) go(std::true_type{});
   else go(std::false_type{});
@@ -405,28 +451,24 @@ hipError_t run_expert_sort(const SortArgs& a) {
 hipError_t run_expert_gather(const RowsArgs& a) {
   if (a.tokens == 0 || a.hidden == 0) return hipSuccess;
   const int64_t esz = a.f32 ? 4 : 2, v = a.f32 ? 4 : 8;
-  const bool vec = a.hidden % v == 0 && vec_ok(a.tok, a.ld_tok, esz) && vec_ok(a.rows, a.ld_rows, esz);
-  by_type(a.f32, vec, [&](auto f32, auto vc) {
-    k_spread<decltype(f32)::value, decltype(vc)::value, false><<<row_grid(a, vec), MT, 0, a.stream>>>(
-        (const char*)a.tok, a.ld_tok, a.hidden, a.pos, a.topk, a.tokens * a.topk, nullptr, 0, (char*)a.rows, a.ld_rows);
+  const bool al = a.hidden % v == 0 && vec_ok(a.tok, a.ld_tok, esz) && vec_ok(a.rows, a.ld_rows, esz);
+  by_type(a.f32, al, [&](auto f32, auto al_) {
+    constexpr bool F32 = decltype(f32)::value, AL = decltype(al_)::value;
+    k_spread<F32, AL><<<row_grid(a), MT, 0, a.stream>>>((const char*)a.tok, a.ld_tok, a.hidden, a.pos, a.topk,
+                                                        a.tokens * a.topk, (char*)a.rows, a.ld_rows);
   });
   return hipGetLastError();
 }
 
 hipError_t run_expert_join(const RowsArgs& a) {
   if (a.tokens == 0 || a.hidden == 0) return hipSuccess;
-  const int64_t esz = a.f32 ? 4 : 2, v = a.f32 ? 4 : 8;
-  const bool vec = a.hidden % v == 0 && vec_ok(a.tok, a.ld_tok, esz) && vec_ok(a.rows, a.ld_rows, esz);
-  by_type(a.f32, vec, [&](auto f32, auto vc) {
-    constexpr bool F32 = decltype(f32)::value, VEC = decltype(vc)::value;
-    if (a.w)
-      k_join<F32, VEC, true><<<row_grid(a, vec), MT, 0, a.stream>>>((const char*)a.rows, a.ld_rows, a.hidden, a.pos,
-                                                                    a.topk, a.tokens * a.topk, a.w, a.ldw,
-                                                                    (char*)a.tok, a.ld_tok);
-    else
-      k_join<F32, VEC, false><<<row_grid(a, vec), MT, 0, a.stream>>>((const char*)a.rows, a.ld_rows, a.hidden, a.pos,
-                                                                     a.topk, a.tokens * a.topk, nullptr, 0,
-                                                                     (char*)a.tok, a.ld_tok);
+  const int64_t esz = a.f32 ? 4 : 2, v = a.f32 ? 4 : 8, n = a.tokens * a.topk;
+  const bool al = a.hidden % v == 0 && vec_ok(a.tok, a.ld_tok, esz) && vec_ok(a.rows, a.ld_rows, esz);
+  by_type(a.f32, al, [&](auto f32, auto al_) {
+    constexpr bool F32 = decltype(f32)::value, AL = decltype(al_)::value;
+    const char* rows = (const char*)a.rows;
+    if (a.w) k_join<F32, AL, true><<<row_grid(a), MT, 0, a.stream>>>(rows, a.ld_rows, a.hidden, a.pos, a.topk, n, a.w, a.ldw, (char*)a.tok, a.ld_tok);
+    else k_join<F32, AL, false><<<row_grid(a), MT, 0, a.stream>>>(rows, a.ld_rows, a.hidden, a.pos, a.topk, n, nullptr, 0, (char*)a.tok, a.ld_tok);
   });
   return hipGetLastError();
 }
@@ -434,21 +476,17 @@ hipError_t run_expert_join(const RowsArgs& a) {
 hipError_t run_expert_combine_grad(const CombineGradArgs& a) {
   if (a.tokens == 0 || (!a.dys && !a.dw)) return hipSuccess;
   const int64_t esz = a.f32 ? 4 : 2, v = a.f32 ? 4 : 8, n = a.tokens * a.topk;
-  const bool vec = a.hidden % v == 0 && vec_ok(a.dy, a.lddy, esz) && (!a.dw || vec_ok(a.ys, a.ldys, esz)) &&
-                   (!a.dys || vec_ok(a.dys, a.lddys, esz));
-  by_type(a.f32, vec, [&](auto f32, auto vc) {
-    constexpr bool F32 = decltype(f32)::value, VEC = decltype(vc)::value;
-    if (a.dys && a.hidden > 0) {
-      RowsArgs r{};
-      r.f32 = a.f32;
-      r.tokens = a.tokens;
-      r.hidden = a.hidden;
-      k_spread<F32, VEC, true><<<row_grid(r, vec), MT, 0, a.stream>>>((const char*)a.dy, a.lddy, a.hidden, a.pos,
-                                                                      a.topk, n, a.w, a.ldw, (char*)a.dys, a.lddys);
-    }
-    if (a.dw)
-      k_slot_dot<F32, VEC><<<(uint32_t)n, MT, 0, a.stream>>>((const char*)a.dy, a.lddy, (const char*)a.ys, a.ldys,
-                                                             a.hidden, a.pos, a.topk, n, a.dw, a.lddw);
+  const bool al = a.hidden % v == 0 && vec_ok(a.dy, a.lddy, esz) && (!a.dw || vec_ok(a.ys, a.ldys, esz)) &&
+                  (!a.dys || vec_ok(a.dys, a.lddys, esz));
+  by_type(a.f32, al, [&](auto f32, auto al_) {
+    constexpr bool F32 = decltype(f32)::value, AL = decltype(al_)::value;
+    auto go = [&](auto r) {
+      constexpr int R = decltype(r)::value;
+      k_combine_grad<F32, AL, R><<<(uint32_t)a.tokens, MT, 0, a.stream>>>((const char*)a.dy, a.lddy, (const char*)a.ys, a.ldys, a.hidden, a.w, a.ldw, a.pos, a.topk, n, (char*)a.dys, a.lddys, a.dw, a.lddw);
+    };
+    if (a.hidden <= MT * v) go(std::integral_constant<int, 1>{});
+    else if (a.hidden <= 2 * MT * v) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 4>{});
   });
   return hipGetLastError();
 }
