@@ -20,13 +20,17 @@ constexpr int SORT_WAVE_SLOTS = 256;     // slots of a wave in the form with one
 constexpr int sort_waves(int E) { return E <= SORT_ONE_EXPERTS ? 16 : 8; }
 
 template <bool ID64>
-__device__ __forceinline__ uint32_t slot_key(const void* ids, int64_t ld, int topk, int64_t slot, int E) {
-  const int64_t t = slot / topk, j = slot - t * topk;
+__device__ __forceinline__ uint32_t slot_key(const void* ids, int64_t ld, int topk, uint32_t slot, int E) {
+  int64_t at = slot;
+  if (ld != topk) {   // rows with a stride
+    const uint32_t t = slot / (uint32_t)topk;
+    at = (int64_t)t * ld + (slot - t * (uint32_t)topk);
+  }
   if constexpr (ID64) {
-    const int64_t id = reinterpret_cast<const int64_t*>(ids)[t * ld + j];
+    const int64_t id = reinterpret_cast<const int64_t*>(ids)[at];
     return id >= 0 && id < E ? (uint32_t)id : (uint32_t)E;
   } else {
-    const int32_t id = reinterpret_cast<const int32_t*>(ids)[t * ld + j];
+    const int32_t id = reinterpret_cast<const int32_t*>(ids)[at];
     return id >= 0 && id < E ? (uint32_t)id : (uint32_t)E;
   }
 }
@@ -62,11 +66,23 @@ __device__ __forceinline__ int block_excl_scan(int v, int* part, int& total) {
   return before + x;
 }
 
-// Counts the keys of slots [lo, hi) into the wave's LDS row.
-template <bool ID64>
-__device__ __forceinline__ void wave_count(const void* ids, int64_t ld, int topk, int E, int64_t lo, int64_t hi,
-                                           int* row) {
-  for (int64_t s = lo + (threadIdx.x & 63); s < hi; s += 64) atomicAdd(&row[slot_key<ID64>(ids, ld, topk, s, E)], 1);
+// The keys of the wave's slots [lo, hi), at most 64 NK of them: lane l's i-th is slot lo + 64 i + l.
+// They are read once, all loads under way together, for both passes over them.
+template <bool ID64, int NK>
+__device__ __forceinline__ void wave_keys(const void* ids, int64_t ld, int topk, int E, int lo, int hi, uint32_t* key) {
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int s = lo + i * 64 + (threadIdx.x & 63);
+    key[i] = s < hi ? slot_key<ID64>(ids, ld, topk, (uint32_t)s, E) : 0u;
+  }
+}
+
+// Counts them into the wave's LDS row.
+template <int NK>
+__device__ __forceinline__ void wave_count(const uint32_t* key, int lo, int hi, int* row) {
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+    if (lo + i * 64 + (int)(threadIdx.x & 63) < hi) atomicAdd(&row[key[i]], 1);
 }
 
 // Keeps the wave's LDS accesses in program order (the LDS itself serves a wave's accesses in order).
@@ -75,15 +91,17 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Places slots [lo, hi): row[key] is the wave's next position of each key.
-template <bool ID64>
-__device__ __forceinline__ void wave_place(const void* ids, int64_t ld, int topk, int E, int bits, int64_t lo,
-                                           int64_t hi, int* row, int32_t* order, int32_t* pos) {
+// Places them: row[key] is the wave's next position of each key.
+template <int NK>
+__device__ __forceinline__ void wave_place(const uint32_t* keys, int E, int bits, int lo, int hi, int* row,
+                                           int32_t* order, int32_t* pos) {
   const int lane = threadIdx.x & 63;
-  for (int64_t b = lo; b < hi; b += 64) {
-    const int64_t s = b + lane;
+#pragma unroll
+  for (int k = 0; k < NK; ++k) {
+    if (lo + k * 64 >= hi) break;
+    const int s = lo + k * 64 + lane;
     const bool ok = s < hi;
-    const uint32_t key = ok ? slot_key<ID64>(ids, ld, topk, s, E) : 0u;
+    const uint32_t key = keys[k];
     uint64_t same = __ballot(ok);
     for (int i = 0; i < bits; ++i) {
       const bool bit = (key >> i) & 1u;
@@ -97,13 +115,13 @@ __device__ __forceinline__ void wave_place(const void* ids, int64_t ld, int topk
     if (ok && rank == 0) row[key] = p + __popcll(same);
     wave_order();
     if (ok) {
-      order[p] = (int32_t)s;
+      order[p] = s;
       pos[s] = key < (uint32_t)E ? p : ~p;
     }
   }
 }
 
-template <bool ID64>
+template <bool ID64, int NK>
 __global__ __launch_bounds__(SORT_ONE_WAVES * 64) void k_sort_one(const void* __restrict__ ids, int64_t ld, int topk,
                                                                   int n, int E, int bits, int32_t* __restrict__ order,
                                                                   int32_t* __restrict__ pos,
@@ -111,11 +129,12 @@ __global__ __launch_bounds__(SORT_ONE_WAVES * 64) void k_sort_one(const void* __
   extern __shared__ int rows[];   // [SORT_ONE_WAVES][E + 1]
   __shared__ int part[SORT_ONE_WAVES];
   const int w = threadIdx.x >> 6, keys = E + 1;
+  const int lo = min(n, w * 64 * NK), hi = min(n, lo + 64 * NK);
+  uint32_t key[NK];
+  wave_keys<ID64, NK>(ids, ld, topk, E, lo, hi, key);
   for (int i = threadIdx.x; i < SORT_ONE_WAVES * keys; i += SORT_ONE_WAVES * 64) rows[i] = 0;
   __syncthreads();
-  const int seg = ((n + SORT_ONE_WAVES * 64 - 1) / (SORT_ONE_WAVES * 64)) * 64;
-  const int lo = min(n, w * seg), hi = min(n, lo + seg);
-  wave_count<ID64>(ids, ld, topk, E, lo, hi, rows + w * keys);
+  wave_count<NK>(key, lo, hi, rows + w * keys);
   __syncthreads();
   // thread t < E: expert t's slots over the waves, its base, then each wave's first position
   const int t = threadIdx.x;
@@ -142,7 +161,7 @@ __global__ __launch_bounds__(SORT_ONE_WAVES * 64) void k_sort_one(const void* __
     }
   }
   __syncthreads();
-  wave_place<ID64>(ids, ld, topk, E, bits, lo, hi, rows + w * keys, order, pos);
+  wave_place<NK>(key, E, bits, lo, hi, rows + w * keys, order, pos);
 }
 
 // counts[chunk][E + 1]
@@ -151,12 +170,14 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_count(const void* __re
                                                                 int n, int E, int32_t* __restrict__ counts) {
   extern __shared__ int rows[];   // [E + 1]
   const int keys = E + 1;
+  constexpr int NK = SORT_WAVE_SLOTS / 64;
+  const int lo = min(n, (int)((blockIdx.x * SORT_WAVES + (threadIdx.x >> 6)) * SORT_WAVE_SLOTS));
+  const int hi = min(n, lo + SORT_WAVE_SLOTS);
+  uint32_t key[NK];
+  wave_keys<ID64, NK>(ids, ld, topk, E, lo, hi, key);
   for (int i = threadIdx.x; i < keys; i += SORT_WAVES * 64) rows[i] = 0;
   __syncthreads();
-  constexpr int CHUNK = SORT_WAVES * SORT_WAVE_SLOTS;
-  const int64_t lo = (int64_t)blockIdx.x * CHUNK, hi = min((int64_t)n, lo + CHUNK);
-  for (int64_t s = lo + threadIdx.x; s < hi; s += SORT_WAVES * 64)
-    atomicAdd(&rows[slot_key<ID64>(ids, ld, topk, s, E)], 1);
+  wave_count<NK>(key, lo, hi, rows);
   __syncthreads();
   for (int i = threadIdx.x; i < keys; i += SORT_WAVES * 64) counts[(int64_t)blockIdx.x * keys + i] = rows[i];
 }
@@ -176,11 +197,13 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_place(const void* __re
   int* total = lds;
   int* before = lds + keys;
   int* rows = lds + 2 * keys;
+  constexpr int NK = SORT_WAVE_SLOTS / 64;
+  const int lo = min(n, (chunk * SORT_WAVES + w) * SORT_WAVE_SLOTS), hi = min(n, lo + SORT_WAVE_SLOTS);
+  uint32_t key[NK];
+  wave_keys<ID64, NK>(ids, ld, topk, E, lo, hi, key);
   for (int i = threadIdx.x; i < (2 + SORT_WAVES) * keys; i += NTH) lds[i] = 0;
   __syncthreads();
-  const int64_t lo = min((int64_t)n, ((int64_t)chunk * SORT_WAVES + w) * SORT_WAVE_SLOTS);
-  const int64_t hi = min((int64_t)n, lo + SORT_WAVE_SLOTS);
-  wave_count<ID64>(ids, ld, topk, E, lo, hi, rows + w * keys);
+  wave_count<NK>(key, lo, hi, rows + w * keys);
   // the keys' columns of counts, `parts` threads to a key when there are few keys
   const int parts = keys >= NTH ? 1 : NTH / keys;
   if (threadIdx.x < parts * keys || keys >= NTH) {
@@ -224,7 +247,7 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_place(const void* __re
     }
   }
   __syncthreads();
-  wave_place<ID64>(ids, ld, topk, E, bits, lo, hi, rows + w * keys, order, pos);
+  wave_place<NK>(key, E, bits, lo, hi, rows + w * keys, order, pos);
 }
 
 // ---------------------------------------------------------------- rows to and from expert order
@@ -429,8 +452,13 @@ hipError_t run_expert_sort(const SortArgs& a) {
   auto go = [&](auto id64) {
     constexpr bool ID64 = decltype(id64)::value;
     if (sort_in_one(n, E)) {
-      k_sort_one<ID64><<<1, SORT_ONE_WAVES * 64, SORT_ONE_WAVES*(E + 1) * sizeof(int), a.stream>>>(
-          a.ids, a.ld_ids, a.topk, n, E, bits, a.order, a.pos, a.offsets);
+      auto one = [&](auto nk) {
+        constexpr int NK = decltype(nk)::value;
+        k_sort_one<ID64, NK><<<1, SORT_ONE_WAVES * 64, SORT_ONE_WAVES * (E + 1) * sizeof(int), a.stream>>>(a.ids, a.ld_ids, a.topk, n, E, bits, a.order, a.pos, a.offsets);
+      };
+      if (n <= SORT_ONE_WAVES * 64) one(std::integral_constant<int, 1>{});
+      else if (n <= SORT_ONE_WAVES * 128) one(std::integral_constant<int, 2>{});
+      else one(std::integral_constant<int, SORT_ONE_MAX / (SORT_ONE_WAVES * 64)>{});
       return;
     }
     int32_t* counts = reinterpret_cast<int32_t*>(a.ws);
