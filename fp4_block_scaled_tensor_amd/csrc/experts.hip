@@ -11,6 +11,8 @@ namespace {
 // key are found with one ballot per key bit, the rank of a lane among them is the population
 // count below it, and the wave keeps its own running position per key in LDS, so ranks follow
 // slot order and no atomic decides an order. Keys are the expert ids; a dropped slot has key E.
+// Bound by latency: one launch up to 8192 slots (32 slots over 8 experts 3.3 us), else a launch that
+// counts and one that places (262144 slots over 128 experts 11.5 us for 3.1 MB).
 constexpr int SORT_ONE_WAVES = 16;       // the one-workgroup form
 constexpr int SORT_ONE_MAX = 8192;       // slots it takes
 constexpr int SORT_ONE_EXPERTS = 512;    // experts it takes (16 LDS rows of E + 1 counters below 64 KiB)
@@ -305,22 +307,28 @@ struct Elems {
 
 constexpr int MT = 256;   // threads of the row kernels
 
+// The three kernels below move rows and are bound by HBM; a workgroup takes a token (its row, and its
+// topk rows in expert order), so each row is read or written once and in order. Measured: gather of
+// 8192 x 2 rows of 4096 bf16 40 us (5.0 TB/s; a plain copy of 1 GiB reaches 5.2), gradient of a
+// gather of 2047 x 4 rows of 1001 float32 8.0 us (5.1 TB/s), both gradients of the combination of
+// 8192 x 2 rows 64 us (5.3 TB/s; 78 us with the weights' gradients in a pass of their own).
+
 // One token's row to its slots' rows (gather): the row is read once and written topk times.
 template <bool F32, bool ALIGNED>
 __global__ __launch_bounds__(MT) void k_spread(const char* __restrict__ x, int64_t ldx, int64_t hidden,
                                                const int32_t* __restrict__ pos, int topk, int64_t n,
-                                               char* __restrict__ xs, int64_t ldxs) {
+                                               char* __restrict__ xs, int64_t ldxs, int64_t tokens) {
   using E = Elems<F32, ALIGNED>;
-  const int64_t t = blockIdx.x;
-  for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
-    float v[E::V], zero[E::V] = {};
-    E::load(x + (t * ldx + h) * E::ESZ, hidden - h, v);
-    for (int j = 0; j < topk; ++j) {
-      const int32_t p = pos[t * topk + j];
-      const int64_t row = p < 0 ? ~p : p;
-      if (row < n) E::store(xs + (row * ldxs + h) * E::ESZ, hidden - h, p < 0 ? zero : v);
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x)
+    for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
+      float v[E::V], zero[E::V] = {};
+      E::load(x + (t * ldx + h) * E::ESZ, hidden - h, v);
+      for (int j = 0; j < topk; ++j) {
+        const int32_t p = pos[t * topk + j];
+        const int64_t row = p < 0 ? ~p : p;
+        if (row < n) E::store(xs + (row * ldxs + h) * E::ESZ, hidden - h, p < 0 ? zero : v);
+      }
     }
-  }
 }
 
 // A token's slots' rows summed, with weights or without.
@@ -328,27 +336,27 @@ template <bool F32, bool ALIGNED, bool WEIGHT>
 __global__ __launch_bounds__(MT) void k_join(const char* __restrict__ ys, int64_t ldys, int64_t hidden,
                                              const int32_t* __restrict__ pos, int topk, int64_t n,
                                              const float* __restrict__ w, int64_t ldw, char* __restrict__ y,
-                                             int64_t ldy) {
+                                             int64_t ldy, int64_t tokens) {
   using E = Elems<F32, ALIGNED>;
-  const int64_t t = blockIdx.x;
-  for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
-    float a[E::V] = {};
-    for (int j = 0; j < topk; ++j) {
-      const int32_t p = pos[t * topk + j];
-      if (p < 0 || p >= n) continue;
-      float v[E::V];
-      E::load(ys + ((int64_t)p * ldys + h) * E::ESZ, hidden - h, v);
-      if constexpr (WEIGHT) {
-        const float f = w[t * ldw + j];
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x)
+    for (int64_t h = ((int64_t)blockIdx.y * MT + threadIdx.x) * E::V; h < hidden; h += (int64_t)gridDim.y * MT * E::V) {
+      float a[E::V] = {};
+      for (int j = 0; j < topk; ++j) {
+        const int32_t p = pos[t * topk + j];
+        if (p < 0 || p >= n) continue;
+        float v[E::V];
+        E::load(ys + ((int64_t)p * ldys + h) * E::ESZ, hidden - h, v);
+        if constexpr (WEIGHT) {
+          const float f = w[t * ldw + j];
 #pragma unroll
-        for (int i = 0; i < E::V; ++i) a[i] = __builtin_fmaf(f, v[i], a[i]);
-      } else {
+          for (int i = 0; i < E::V; ++i) a[i] = __builtin_fmaf(f, v[i], a[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < E::V; ++i) a[i] += v[i];
+          for (int i = 0; i < E::V; ++i) a[i] += v[i];
+        }
       }
+      E::store(y + (t * ldy + h) * E::ESZ, hidden - h, a);
     }
-    E::store(y + (t * ldy + h) * E::ESZ, hidden - h, a);
-  }
 }
 
 // Gradient of the weighted sum: a workgroup takes a token's dy, scales it into its slots' rows of
@@ -361,62 +369,64 @@ __global__ __launch_bounds__(MT) void k_combine_grad(const char* __restrict__ dy
                                                      const float* __restrict__ w, int64_t ldw,
                                                      const int32_t* __restrict__ pos, int topk, int64_t n,
                                                      char* __restrict__ dys, int64_t lddys, float* __restrict__ dw,
-                                                     int64_t lddw) {
+                                                     int64_t lddw, int64_t tokens) {
   using E = Elems<F32, ALIGNED>;
   constexpr int STEP = MT * E::V;
   __shared__ float part[JB][MT / 64];
-  const int64_t t = blockIdx.x, h0 = (int64_t)threadIdx.x * E::V;
-  float u[R][E::V];
+  const int64_t h0 = (int64_t)threadIdx.x * E::V;
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    float u[R][E::V];
 #pragma unroll
-  for (int c = 0; c < R; ++c) {
-    const int64_t h = h0 + c * STEP;
-    if (h < hidden) {
-      E::load(dy + (t * lddy + h) * E::ESZ, hidden - h, u[c]);
-    } else {
+    for (int c = 0; c < R; ++c) {
+      const int64_t h = h0 + c * STEP;
+      if (h < hidden) {
+        E::load(dy + (t * lddy + h) * E::ESZ, hidden - h, u[c]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < E::V; ++i) u[c][i] = 0.0f;
-    }
-  }
-  for (int j0 = 0; j0 < topk; j0 += JB) {
-    const int jn = min(JB, topk - j0);
-    for (int j = 0; j < jn; ++j) {
-      const int32_t p = pos[t * topk + j0 + j];
-      const int64_t row = p < 0 ? ~p : p;
-      const bool kept = p >= 0 && row < n;
-      float a = 0.0f;
-      if (row < n) {
-        const float f = kept && dys ? w[t * ldw + j0 + j] : 0.0f;
-        auto chunk = [&](int64_t h, const float* g) {
-          if (dys) {
-            float o[E::V];
-#pragma unroll
-            for (int i = 0; i < E::V; ++i) o[i] = kept ? f * g[i] : 0.0f;
-            E::store(dys + (row * lddys + h) * E::ESZ, hidden - h, o);
-          }
-          if (kept && dw) {
-            float v[E::V];
-            E::load(ys + (row * ldys + h) * E::ESZ, hidden - h, v);
-#pragma unroll
-            for (int i = 0; i < E::V; ++i) a = __builtin_fmaf(g[i], v[i], a);
-          }
-        };
-#pragma unroll
-        for (int c = 0; c < R; ++c)
-          if (h0 + c * STEP < hidden) chunk(h0 + c * STEP, u[c]);
-        for (int64_t h = h0 + R * STEP; h < hidden; h += STEP) {
-          float g[E::V];
-          E::load(dy + (t * lddy + h) * E::ESZ, hidden - h, g);
-          chunk(h, g);
-        }
+        for (int i = 0; i < E::V; ++i) u[c][i] = 0.0f;
       }
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) a += __shfl_xor(a, o, 64);
-      if ((threadIdx.x & 63) == 0) part[j][threadIdx.x >> 6] = a;
     }
-    __syncthreads();
-    if (dw && threadIdx.x < jn)
-      dw[t * lddw + j0 + threadIdx.x] = (part[threadIdx.x][0] + part[threadIdx.x][1]) + (part[threadIdx.x][2] + part[threadIdx.x][3]);
-    __syncthreads();
+    for (int j0 = 0; j0 < topk; j0 += JB) {
+      const int jn = min(JB, topk - j0);
+      for (int j = 0; j < jn; ++j) {
+        const int32_t p = pos[t * topk + j0 + j];
+        const int64_t row = p < 0 ? ~p : p;
+        const bool kept = p >= 0 && row < n;
+        float a = 0.0f;
+        if (row < n) {
+          const float f = kept && dys ? w[t * ldw + j0 + j] : 0.0f;
+          auto chunk = [&](int64_t h, const float* g) {
+            if (dys) {
+              float o[E::V];
+#pragma unroll
+              for (int i = 0; i < E::V; ++i) o[i] = kept ? f * g[i] : 0.0f;
+              E::store(dys + (row * lddys + h) * E::ESZ, hidden - h, o);
+            }
+            if (kept && dw) {
+              float v[E::V];
+              E::load(ys + (row * ldys + h) * E::ESZ, hidden - h, v);
+#pragma unroll
+              for (int i = 0; i < E::V; ++i) a = __builtin_fmaf(g[i], v[i], a);
+            }
+          };
+#pragma unroll
+          for (int c = 0; c < R; ++c)
+            if (h0 + c * STEP < hidden) chunk(h0 + c * STEP, u[c]);
+          for (int64_t h = h0 + R * STEP; h < hidden; h += STEP) {
+            float g[E::V];
+            E::load(dy + (t * lddy + h) * E::ESZ, hidden - h, g);
+            chunk(h, g);
+          }
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) a += __shfl_xor(a, o, 64);
+        if ((threadIdx.x & 63) == 0) part[j][threadIdx.x >> 6] = a;
+      }
+      __syncthreads();
+      if (dw && threadIdx.x < jn)
+        dw[t * lddw + j0 + threadIdx.x] = (part[threadIdx.x][0] + part[threadIdx.x][1]) + (part[threadIdx.x][2] + part[threadIdx.x][3]);
+      __syncthreads();
+    }
   }
 }
 
@@ -433,8 +443,11 @@ void by_type(bool f32, bool vec, F&& f) {
   else vec ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
 }
 
+// workgroups over tokens: a grid holds less than 2^32 threads, so past this many each takes several
+uint32_t token_grid(int64_t tokens) { return (uint32_t)std::min<int64_t>(tokens, int64_t(1) << 22); }
+
 dim3 row_grid(const RowsArgs& a) {
-  return dim3((uint32_t)a.tokens, (uint32_t)std::min<int64_t>(div_up(a.hidden, MT * (a.f32 ? 4 : 8)), 1024));
+  return dim3(token_grid(a.tokens), (uint32_t)std::min<int64_t>(div_up(a.hidden, MT * (a.f32 ? 4 : 8)), 1024));
 }
 
 bool sort_in_one(int64_t n, int E) { return n <= SORT_ONE_MAX && E <= SORT_ONE_EXPERTS; }
@@ -483,7 +496,7 @@ hipError_t run_expert_gather(const RowsArgs& a) {
   by_type(a.f32, al, [&](auto f32, auto al_) {
     constexpr bool F32 = decltype(f32)::value, AL = decltype(al_)::value;
     k_spread<F32, AL><<<row_grid(a), MT, 0, a.stream>>>((const char*)a.tok, a.ld_tok, a.hidden, a.pos, a.topk,
-                                                        a.tokens * a.topk, (char*)a.rows, a.ld_rows);
+                                                        a.tokens * a.topk, (char*)a.rows, a.ld_rows, a.tokens);
   });
   return hipGetLastError();
 }
@@ -495,8 +508,8 @@ hipError_t run_expert_join(const RowsArgs& a) {
   by_type(a.f32, al, [&](auto f32, auto al_) {
     constexpr bool F32 = decltype(f32)::value, AL = decltype(al_)::value;
     const char* rows = (const char*)a.rows;
-    if (a.w) k_join<F32, AL, true><<<row_grid(a), MT, 0, a.stream>>>(rows, a.ld_rows, a.hidden, a.pos, a.topk, n, a.w, a.ldw, (char*)a.tok, a.ld_tok);
-    else k_join<F32, AL, false><<<row_grid(a), MT, 0, a.stream>>>(rows, a.ld_rows, a.hidden, a.pos, a.topk, n, nullptr, 0, (char*)a.tok, a.ld_tok);
+    if (a.w) k_join<F32, AL, true><<<row_grid(a), MT, 0, a.stream>>>(rows, a.ld_rows, a.hidden, a.pos, a.topk, n, a.w, a.ldw, (char*)a.tok, a.ld_tok, a.tokens);
+    else k_join<F32, AL, false><<<row_grid(a), MT, 0, a.stream>>>(rows, a.ld_rows, a.hidden, a.pos, a.topk, n, nullptr, 0, (char*)a.tok, a.ld_tok, a.tokens);
   });
   return hipGetLastError();
 }
@@ -510,7 +523,7 @@ hipError_t run_expert_combine_grad(const CombineGradArgs& a) {
     constexpr bool F32 = decltype(f32)::value, AL = decltype(al_)::value;
     auto go = [&](auto r) {
       constexpr int R = decltype(r)::value;
-      k_combine_grad<F32, AL, R><<<(uint32_t)a.tokens, MT, 0, a.stream>>>((const char*)a.dy, a.lddy, (const char*)a.ys, a.ldys, a.hidden, a.w, a.ldw, a.pos, a.topk, n, (char*)a.dys, a.lddys, a.dw, a.lddw);
+      k_combine_grad<F32, AL, R><<<token_grid(a.tokens), MT, 0, a.stream>>>((const char*)a.dy, a.lddy, (const char*)a.ys, a.ldys, a.hidden, a.w, a.ldw, a.pos, a.topk, n, (char*)a.dys, a.lddys, a.dw, a.lddw, a.tokens);
     };
     if (a.hidden <= MT * v) go(std::integral_constant<int, 1>{});
     else if (a.hidden <= 2 * MT * v) go(std::integral_constant<int, 2>{});
