@@ -306,6 +306,27 @@ def test_linear(fmt, block, layout, dtype, out):
         close(y, x.cpu().double().numpy(), w64, float(np.float32(0.37)), DT[out], f"{m}x{n}x{k}")
 
 
+# Sizes that take every kernel shape: few rows with one, two and four products to a fragment and 4, 8 and 16 rows
+# at a time; tiles of 32 to 256 rows, with and without a split K. K = 192 and 320 end half way into a turn.
+SHAPES = [(1, 8208, 192), (3, 16400, 192), (7, 8208, 320), (8, 16400, 128), (12, 16400, 192), (16, 8208, 192),
+          (20, 4112, 1088), (100, 32784, 192), (90, 16400, 320), (50, 65616, 64), (2045, 6160, 192), (1030, 8208, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,block,layout", [("ue5m3", 16, "1d"), ("e4m3", 16, "2dT"), ("e4m3", 32, "1d"), ("e8m0", 32, "1d")])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear_every_shape(shape, fmt, block, layout, dtype):
+    """Exact on integers (quantum 2^-6, sums below 2^18), in float64 on the device."""
+    import fp4_block_scaled_tensor_amd as fp4
+    m, n, k = shape
+    r = gen(m + n)
+    w, _ = random_weight(r, n, k, fmt, block, layout, spread=1)
+    x = torch.from_numpy(r.integers(-8, 9, (m, k)).astype(np.float32)).to(DT[dtype]).cuda()
+    y = fp4.linear(x, w, out_dtype=torch.float32)
+    want = x.double() @ fp4.dequantize(w).double().t().contiguous()
+    assert torch.equal(y.double(), want)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("fmt,block,layout", WEIGHTS)
 def test_linear_exact_on_integers(fmt, block, layout, dtype):
@@ -424,7 +445,7 @@ def test_linear_transposed_view_is_the_gradient():
 EXPERT_CASES = [
     # rows of each expert, dropped rows
     ([1], 0), ([0, 0, 3, 0], 0), ([2, 1, 0, 5, 4, 0, 1, 1], 2), ([40, 0, 7, 129], 5), ([0, 300, 1, 17], 0),
-    ([64] * 6, 0), ([0, 0], 9), ([513, 2, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0], 1), ([256, 255, 257], 3),
+    ([64] * 6, 0), ([0, 0], 9), ([0] * 30 + [200] + [1] * 33, 4), ([1] * 70 + [30], 0), ([3] * 130 + [0], 1), ([513, 2, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0], 1), ([256, 255, 257], 3),
 ]
 
 
@@ -450,6 +471,22 @@ def test_expert_linear(fmt, block, layout, dtype):
             if counts[e]:
                 a, b = int(ends[e]), int(ends[e + 1])
                 close(out[a:b], x[a:b].cpu().double().numpy(), pairs[e][1], 0.5 + e, torch.float32, f"case {i} expert {e}")
+
+
+@pytest.mark.parametrize("fmt,block,layout", [("ue5m3", 16, "1d"), ("e4m3", 16, "2dT"), ("e8m0", 32, "1d")])
+@pytest.mark.parametrize("counts,n", [([1000, 1, 0, 1044], 6160), ([2, 0, 1, 0, 3], 8208), ([40, 30, 0, 50], 16400)])
+def test_expert_linear_large(counts, n, fmt, block, layout):
+    """Tall tiles and wide weights over experts, exact on integers."""
+    import fp4_block_scaled_tensor_amd as fp4
+    r, k = gen(n), 192
+    ws = [random_weight(r, n, k, fmt, block, layout, spread=1)[0] for _ in counts]
+    ends = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    x = torch.from_numpy(r.integers(-8, 9, (int(ends[-1]) + 3, k)).astype(np.float32)).to(torch.bfloat16).cuda()
+    y = fp4.expert_linear(x, fp4.stack_experts(ws), torch.from_numpy(ends).cuda(), out_dtype=torch.float32)
+    assert (y[int(ends[-1]):] == 0).all()
+    for e, w in enumerate(ws):
+        a, b = int(ends[e]), int(ends[e + 1])
+        assert torch.equal(y[a:b].double(), x[a:b].double() @ fp4.dequantize(w).double().t().contiguous()), e
 
 
 def test_expert_linear_bad_offsets_stay_in_bounds():
