@@ -59,8 +59,6 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
 }
-template <class T>
-__device__ __forceinline__ void pin(T& v) { asm volatile("" : "+v"(v)); }
 // this wave's copies have landed and its LDS reads are done
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
@@ -70,16 +68,9 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// the value of a scale code
-template <int FMT>
-__device__ __forceinline__ float wscale(uint32_t c) {
-  if constexpr (FMT == FMT_E8M0) return c ? __uint_as_float(c << 23) : __uint_as_float(1u << 22);
-  else return dec_scale3<FMT>(c);
-}
-
-template <int FMT, int SEL>
+template <bool E8, int SEL>
 __device__ __forceinline__ uint32_t decode_pair(uint32_t w, float sv) {
-  if constexpr (FMT == FMT_E8M0) {
+  if constexpr (E8) {
     // the conversion applies the scale's power of two
     typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
     const v2bf v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sv, SEL);
@@ -91,10 +82,10 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w, float sv) {
 }
 
 // 8 codes (one dword, element 0 in the low nibble) times their scale -> 8 bf16, exact
-template <int FMT>
+template <bool E8>
 __device__ __forceinline__ v8bf decode8_bf16(uint32_t w, float sv) {
-  const v4u r = {decode_pair<FMT, 0>(w, sv), decode_pair<FMT, 1>(w, sv), decode_pair<FMT, 2>(w, sv),
-                 decode_pair<FMT, 3>(w, sv)};
+  const v4u r = {decode_pair<E8, 0>(w, sv), decode_pair<E8, 1>(w, sv), decode_pair<E8, 2>(w, sv),
+                 decode_pair<E8, 3>(w, sv)};
   return __builtin_bit_cast(v8bf, r);
 }
 
@@ -162,11 +153,12 @@ struct FormArgs {
   int s_band;            // log2 of the rows that share a scale row (0 or 4)
 };
 
-// E8: power-of-two scales; else 3 mantissa bits: the code's bits as a float32 times 2^(127 - bias),
-// subnormals included
+// The value of a scale code. E8: 2^(c - 127). Else 3 mantissa bits: the code's bits as a float32 times
+// 2^(127 - bias), subnormals included.
 template <bool E8>
 __device__ __forceinline__ float code_value(uint32_t c, float scale_mul) {
-  return E8 ? wscale<FMT_E8M0>(c) : __uint_as_float(c << 20) * scale_mul;
+  if constexpr (E8) return c ? __uint_as_float(c << 23) : __uint_as_float(1u << 22);
+  else return __uint_as_float(c << 20) * scale_mul;
 }
 
 // ---------------------------------------------------------------- weight turns
@@ -261,6 +253,8 @@ struct WeightTurns {
 // turns are in flight while one is multiplied. Activation rows past the group repeat its last one;
 // their products, and those of the 16 - XR rows of a product that are not there, are not stored.
 // Activation row r (256 bytes) keeps its 16-byte piece j at j ^ r % 16, against bank conflicts.
+// Measured: 114688 x 4096 MXFP4, one row, 54 us (4.6 TB/s); 28672 x 4096 18.6 us, 5 to 6 us of it launch
+// and ramp; 4096 x 4096 4.5 us. Three-mantissa-bit scales add the decode, 28672 x 4096 UE5M3 23 us.
 template <bool E8_, int B_, int PLANES_, int TN_, int XR_, bool BYTES_>
 struct RowsForm {
   static constexpr bool E8 = E8_, BYTES = BYTES_;
@@ -276,8 +270,8 @@ struct RowsForm {
 
 template <class F>
 __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs t) {
-  constexpr bool E8 = F::E8, BYTES = F::BYTES;
-  constexpr int B = F::B, PLANES = F::PLANES, TN = F::TN, XR = F::XR, NW = F::NW, D = F::D;
+  constexpr bool E8 = F::E8;
+  constexpr int PLANES = F::PLANES, TN = F::TN, XR = F::XR, NW = F::NW, D = F::D;
   __shared__ __attribute__((aligned(1024))) char lds[NW * D * F::TURN];
   const int e = blockIdx.y, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kg = lane >> 4;
@@ -362,7 +356,7 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           const float sv = code_value<E8>(sc[j][d / 2], t.scale_mul);
-          const v8bf b = decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(w[j][d], sv);
+          const v8bf b = decode8_bf16<E8>(w[j][d], sv);
 #pragma unroll
           for (int o = 0; o < PLANES; ++o)
             acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x[o][d]), b, acc[j], 0, 0, 0);
@@ -395,13 +389,16 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
 
 // ---------------------------------------------------------------- tile form
 // A workgroup owns a BM x 256 tile of one expert's outputs: four waves, each all BM = 32 TM rows of
-// x and 64 of the weight's rows (TM x 2 products of 32x32x16). K advances in steps of 64.
+// x and 64 of the weight's rows (TM x 2 products of 32x32x16), or for BM = 256 eight waves with 32 of
+// the weight's rows each, two to a SIMD. K advances in steps of 64. Bound by the matrix cores, which
+// are busy 66% of the cycles (8192 rows over eight experts, 4096 -> 14336, MXFP4: 0.92 ms; a plain
+// 8192 x 4096 -> 14336 product 758 us, 1.27 PFLOP/s, the library's bf16 product 650 us).
 //
 // A wave needs its weight rows for itself alone, so it copies their codes and scales a turn of 128 k
 // at a time and decodes them in registers: lane l holds row l % 32 and the 32 codes of K half l / 32
 // of a step, which feed four products (the order of k inside a step is free as long as both operands
 // agree). The rows of x, which every wave needs, are copied into LDS a step at a time, NXB steps
-// deep. Staging the decoded weight in LDS instead, with 128 x 64 outputs to a wave, was slower: 1.24
+// deep (NXB below). Staging the decoded weight in LDS instead, with 128 x 64 outputs to a wave, was slower: 1.24
 // ms against 0.96 for 8192 rows of eight experts, 4096 -> 14336.
 //
 // Fragments are read one product group ahead. The barrier of a step stands before its last group:
@@ -489,7 +486,7 @@ struct TileForm {
 template <class F>
 __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileArgs t) {
   constexpr bool E8 = F::E8;
-  constexpr int B = F::B, PLANES = F::PLANES, TM = F::TM, TN = F::TN, TILE_NW = F::NW, BM = F::BM, STAGE = F::STAGE;
+  constexpr int PLANES = F::PLANES, TM = F::TM, TN = F::TN, TILE_NW = F::NW, BM = F::BM, STAGE = F::STAGE;
   constexpr int PIECES = F::PIECES, OW = F::OW, OLD = F::OLD, NXB = F::NXB;
   __shared__ __attribute__((aligned(1024))) char lds[F::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -567,7 +564,7 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
   };
   auto decode = [&](int i, int s) {   // dword s: k = 32 (lane / 32) + 8 s ..
     const float sv = code_value<E8>(sc[i][s / 2], t.f.scale_mul);
-    return decode8_bf16<E8 ? FMT_E8M0 : FMT_UE5M3>(codes[i][s], sv);
+    return decode8_bf16<E8>(codes[i][s], sv);
   };
 
   v16f acc[TN][TM];
