@@ -121,6 +121,13 @@ def _linear_workspace(rows: int, dtype: int, fmt: int, block: int, layout: int, 
     return ws.value
 
 
+def _address(workspace: torch.Tensor | None) -> int | None:
+    """A workspace's address. The caller keeps the tensor in a local until the library call has
+    returned: only then is everything enqueued that uses it, and a block that is dropped before may
+    be given to another thread (the call releases the interpreter lock) or be unmapped."""
+    return None if workspace is None else workspace.data_ptr()
+
+
 def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
     """fp4_expert_sort: the plan of ids [tokens, topk] (int32 or int64; an id outside
     [0, n_experts) drops its slot)."""
@@ -135,9 +142,10 @@ def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
     order = torch.empty(n, dtype=torch.int32, device=dev)
     pos = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
     offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
-    work = torch.empty(nb, dtype=torch.uint8, device=dev).data_ptr() if nb else None
+    work = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
     _lib.check(lib.fp4_expert_sort(ids.data_ptr(), int(ids.dtype is torch.int64), tokens, topk, ld, n_experts,
-                                   order.data_ptr(), pos.data_ptr(), offsets.data_ptr(), work, nb, _stream_of(ids)))
+                                   order.data_ptr(), pos.data_ptr(), offsets.data_ptr(), _address(work), nb,
+                                   _stream_of(ids)))
     return ExpertPlan(order, pos, offsets, tokens, topk, n_experts)
 
 
@@ -208,7 +216,7 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
 
 
 def _product(x, w, rows, n_experts, out_dtype, out):
-    """What linear and expert_linear share: checks, output, workspace."""
+    """What linear and expert_linear share: checks, output, workspace (a tensor to hold, see _address)."""
     ldx = _ld("x", x, rows, w.k, x.dtype)
     dt = _dtype(x, "x")
     if out is None:
@@ -218,7 +226,7 @@ def _product(x, w, rows, n_experts, out_dtype, out):
         ldo = _ld("out", out, rows, w.rows, out_dtype or out.dtype)
     odt = _dtype(out, "out")
     nb = _linear_workspace(rows, dt, w.fmt, w.block, w.layout, w.g_stripe, w.rows, w.k, n_experts)
-    ws = x.new_empty(nb, dtype=torch.uint8).data_ptr() if nb else None
+    ws = x.new_empty(nb, dtype=torch.uint8) if nb else None
     return ldx, dt, out, ldo, odt, ws, nb
 
 
@@ -232,8 +240,8 @@ def linear(x: torch.Tensor, w: QTensor, out_dtype=None, out: torch.Tensor | None
     ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, 0, out_dtype, out)
     _dev_check(w.q)
     op = w.operand()
-    _lib.check(lib.fp4_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), out.data_ptr(), odt, ldo, ws, nb,
-                              _stream_of(x)))
+    _lib.check(lib.fp4_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), out.data_ptr(), odt, ldo, _address(ws),
+                              nb, _stream_of(x)))
     return out
 
 
@@ -253,5 +261,5 @@ def expert_linear(x: torch.Tensor, w: ExpertWeights, plan: ExpertPlan | torch.Te
     _dev_check(w.q, offsets)
     op = w.operand()
     _lib.check(lib.fp4_expert_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), experts, offsets.data_ptr(),
-                                     out.data_ptr(), odt, ldo, ws, nb, _stream_of(x)))
+                                     out.data_ptr(), odt, ldo, _address(ws), nb, _stream_of(x)))
     return out
