@@ -166,6 +166,11 @@ __global__ __launch_bounds__(SORT_ONE_WAVES * 64) void k_sort_one(const void* __
   wave_place<NK>(key, E, bits, lo, hi, rows + w * keys, order, pos);
 }
 
+// no slots: the experts' offsets alone
+__global__ __launch_bounds__(256) void k_sort_none(int E, int32_t* __restrict__ offsets) {
+  for (int i = threadIdx.x; i <= E; i += 256) offsets[i] = 0;
+}
+
 // counts[chunk][E + 1]
 template <bool ID64, int SORT_WAVES>
 __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_count(const void* __restrict__ ids, int64_t ld, int topk,
@@ -462,6 +467,10 @@ hipError_t run_expert_sort(const SortArgs& a) {
   const int n = (int)(a.tokens * a.topk), E = a.n_experts;
   int bits = 0;
   while ((E >> bits) != 0) ++bits;   // keys 0 .. E
+  if (n == 0) {   // no chunk to launch a workgroup for
+    k_sort_none<<<1, 256, 0, a.stream>>>(E, a.offsets);
+    return hipGetLastError();
+  }
   auto go = [&](auto id64) {
     constexpr bool ID64 = decltype(id64)::value;
     if (sort_in_one(n, E)) {
