@@ -464,7 +464,7 @@ struct TileArgs {
   FormArgs f;
   uint32_t mtiles, ntiles;   // mtiles: an upper bound with offsets
   int slices;                // parts of K, each with its own output rows in `part`
-  float* part;               // [slices][rows][N] sums of a split K, or null: write y
+  float* part;               // [slices][rows][N] sums of a split K (without g), or null: write y
 };
 
 // E8: power-of-two scales (block 32), else 3-mantissa-bit ones with block B. PLANES: bf16 parts of x.
@@ -654,7 +654,8 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
   // Each wave turns 32 rows of its columns at a time through its own LDS rows.
   float* out = reinterpret_cast<float*>(lds) + wave * 32 * OLD;
   const int64_t c0 = n0 + wave * OW;
-  const float* g = p.g ? p.g + (int64_t)e * p.g_stride : nullptr;
+  // parts of a split K are joined before g multiplies them
+  const float* g = p.g && !t.part ? p.g + (int64_t)e * p.g_stride : nullptr;
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
 #pragma unroll
@@ -689,15 +690,30 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
   }
 }
 
-// The slices' sums in slice order, rounded once to y's type; V = 4 columns at a time where rows of y
-// and N allow it: 48 x 4096 -> 14336 bf16 33.9 -> 31.5 us, 200 x 14336 -> 4096 bf16 49.9 -> 46.5 us,
+// The group of a row: the last whose rows start at or before it.
+__device__ __forceinline__ int group_of(const WParams& p, int64_t row) {
+  int lo = 0, hi = p.n_experts;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (p.offsets[mid] <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The slices' sums in slice order, times g, rounded once to y's type; V = 4 columns at a time where rows
+// of y and N allow it: 48 x 4096 -> 14336 bf16 33.9 -> 31.5 us, 200 x 14336 -> 4096 bf16 49.9 -> 46.5 us,
 // 128 x 4096 -> 14336 float32 64.1 -> 62.5 us for the whole product, one column at a time against four.
 template <bool YF32, int V>
-__global__ __launch_bounds__(256) void k_join_slices(const float* __restrict__ part, int slices, int64_t rows, int64_t N,
-                                                     char* __restrict__ y, int64_t ldy) {
-  const int64_t n = rows * N, per = N / V;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
-    const int64_t at = i / per * ldy + i % per * V;
+__global__ __launch_bounds__(256) void k_join_slices(const float* __restrict__ part, int slices, WParams p) {
+  const int64_t n = p.rows * p.N, per = p.N / V;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.rows * per; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per, col = i % per * V, at = row * p.ldy + col;
+    float g = 1.0f;   // V columns share it: stripes are multiples of 16 columns
+    if (p.g) {
+      const int e = p.offsets ? group_of(p, row) : 0;
+      if (e < p.n_experts) g = p.g[(int64_t)e * p.g_stride + (p.g_shift ? col >> p.g_shift : 0)];   // else zeros
+    }
     if constexpr (V == 4) {
       v4f v = *reinterpret_cast<const v4f*>(part + i * 4);
       for (int s = 1; s < slices; ++s) {
@@ -705,12 +721,14 @@ __global__ __launch_bounds__(256) void k_join_slices(const float* __restrict__ p
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += u[j];
       }
-      if constexpr (YF32) *reinterpret_cast<v4f*>(y + at * 4) = v;
-      else *reinterpret_cast<uint64_t*>(y + at * 2) = (uint64_t)pack_bf16(v[2], v[3]) << 32 | pack_bf16(v[0], v[1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= g;
+      if constexpr (YF32) *reinterpret_cast<v4f*>(p.y + at * 4) = v;
+      else *reinterpret_cast<uint64_t*>(p.y + at * 2) = (uint64_t)pack_bf16(v[2], v[3]) << 32 | pack_bf16(v[0], v[1]);
     } else {
       float v = part[i];
       for (int s = 1; s < slices; ++s) v += part[s * n + i];
-      store1<YF32>(y, at, v);
+      store1<YF32>(p.y, at, v * g);
     }
   }
 }
@@ -842,7 +860,7 @@ void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
       constexpr bool YF32 = decltype(f32)::value;
       constexpr int V = decltype(v)::value;
       const uint32_t join_grid = (uint32_t)std::min<int64_t>(div_up(a.rows * a.N / V, 256), 4096);
-      k_join_slices<YF32, V><<<join_grid, 256, 0, a.stream>>>(t.part, t.slices, a.rows, a.N, (char*)a.y, a.ldy);
+      k_join_slices<YF32, V><<<join_grid, 256, 0, a.stream>>>(t.part, t.slices, p);
     };
     const bool vec = f.y_vec && a.N % 4 == 0;
     auto typed = [&](auto f32) {
