@@ -98,6 +98,17 @@ def _ld(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype) -
     return stride[0] if rows > 1 else width
 
 
+def _pos(plan: ExpertPlan, like: torch.Tensor) -> int:
+    """The address of a plan's positions, which the kernels read as packed int32 on like's device
+    (the rows' own checks do not cover them, and plans are also built by callers)."""
+    pos = plan.pos
+    if (pos.dtype is not torch.int32 or pos.numel() != plan.tokens * plan.topk or not pos.is_contiguous()
+            or pos.device != like.device):
+        raise ValueError(f"plan.pos must be a contiguous int32 tensor [{plan.tokens}, {plan.topk}] on {like.device}, got "
+                         f"{pos.dtype} {tuple(pos.shape)} on {pos.device}")
+    return pos.data_ptr()
+
+
 def _width(name: str, t: torch.Tensor) -> int:
     shape = t.shape
     if len(shape) != 2:
@@ -160,7 +171,7 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = 
         out, ldo = x.new_empty((n, h)), h
     else:
         ldo = _ld("out", out, n, h, x.dtype)
-    _lib.check(lib.fp4_expert_gather(x.data_ptr(), dt, plan.tokens, h, ldx, plan.pos.data_ptr(), plan.topk,
+    _lib.check(lib.fp4_expert_gather(x.data_ptr(), dt, plan.tokens, h, ldx, _pos(plan, x), plan.topk,
                                      out.data_ptr(), ldo, _stream_of(x)))
     return out
 
@@ -175,7 +186,7 @@ def expert_gather_grad(dxs: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | 
         out, ldo = dxs.new_empty((plan.tokens, h)), h
     else:
         ldo = _ld("out", out, plan.tokens, h, dxs.dtype)
-    _lib.check(lib.fp4_expert_gather_grad(dxs.data_ptr(), dt, plan.tokens, h, ld, plan.pos.data_ptr(), plan.topk,
+    _lib.check(lib.fp4_expert_gather_grad(dxs.data_ptr(), dt, plan.tokens, h, ld, _pos(plan, dxs), plan.topk,
                                           out.data_ptr(), ldo, _stream_of(dxs)))
     return out
 
@@ -194,7 +205,7 @@ def expert_combine(ys: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     else:
         ldo = _ld("out", out, plan.tokens, h, ys.dtype)
     _lib.check(lib.fp4_expert_combine(ys.data_ptr(), dt, plan.tokens, h, ld, weights.data_ptr(), ldw,
-                                      plan.pos.data_ptr(), plan.topk, out.data_ptr(), ldo, _stream_of(ys)))
+                                      _pos(plan, ys), plan.topk, out.data_ptr(), ldo, _stream_of(ys)))
     return out
 
 
@@ -210,7 +221,7 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
     dys = dy.new_empty((n, h))
     dw = weights.new_empty((plan.tokens, plan.topk))
     _lib.check(lib.fp4_expert_combine_grad(dy.data_ptr(), dt, plan.tokens, h, lddy, ys.data_ptr(), ldys,
-                                           weights.data_ptr(), ldw, plan.pos.data_ptr(), plan.topk, dys.data_ptr(), h,
+                                           weights.data_ptr(), ldw, _pos(plan, dy), plan.topk, dys.data_ptr(), h,
                                            dw.data_ptr(), plan.topk, _stream_of(dy)))
     return dys, dw
 
@@ -249,16 +260,20 @@ def expert_linear(x: torch.Tensor, w: ExpertWeights, plan: ExpertPlan | torch.Te
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_linear: rows x [rows, k] in expert order, each times its expert's weight
     transposed, [rows, n] in out_dtype (x's by default). plan: an ExpertPlan or its offsets (int32
-    [n_experts + 1] on the device); rows past the last offset give zeros."""
+    [n_experts + 1] on x's device); rows past the last offset give zeros. With an ExpertPlan x has its
+    tokens * topk rows, with offsets any number of at least the last one."""
     lib = _lib.load()
     offsets = plan.offsets if isinstance(plan, ExpertPlan) else plan
     experts = w.n_experts
-    if offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous():
-        raise ValueError(f"offsets must be a contiguous int32 tensor of {experts + 1} elements")
     _width("x", x)
     rows = x.shape[0]
+    if (offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous()
+            or offsets.device != x.device):
+        raise ValueError(f"offsets must be a contiguous int32 tensor of {experts + 1} elements on {x.device}")
+    if isinstance(plan, ExpertPlan) and rows != plan.tokens * plan.topk:
+        raise ValueError(f"x must have the plan's {plan.tokens * plan.topk} rows (tokens * topk), got {rows}")
     ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, experts, out_dtype, out)
-    _dev_check(w.q, offsets)
+    _dev_check(w.q)
     op = w.operand()
     _lib.check(lib.fp4_expert_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), experts, offsets.data_ptr(),
                                      out.data_ptr(), odt, ldo, _address(ws), nb, _stream_of(x)))
