@@ -308,6 +308,7 @@ def test_linear(fmt, block, layout, dtype, out):
 
 # Sizes that take every kernel shape: few rows with one, two and four products to a fragment and 4, 8 and 16 rows
 # at a time; tiles of 32 to 256 rows, with and without a split K. K = 192 and 320 end half way into a turn.
+# (With a split K these are 32-row tiles; test_gpu_wlinear_split.py takes the taller ones.)
 SHAPES = [(1, 8208, 192), (3, 16400, 192), (7, 8208, 320), (8, 16400, 128), (12, 16400, 192), (16, 8208, 192),
           (20, 4112, 1088), (100, 32784, 192), (90, 16400, 320), (50, 65616, 64), (2045, 6160, 192), (1030, 8208, 128)]
 

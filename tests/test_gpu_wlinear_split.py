@@ -59,3 +59,57 @@ def test_each_rows_expert_gives_its_g(n, stripe):
         for r in range(ends[e], ends[e] + c):
             want[r] = np.float32(r + 1) * (np.repeat(v, stripe)[:n] if stripe else np.repeat(v, n))
     assert np.array_equal(y, want)
+
+
+# Sizes whose K is split, and the tile heights they take on 256 compute units: 32, 64, 96, 128 and 256 rows. 19
+# steps of K: the parts begin at even and at odd turns of two steps, and the last turn is half a turn.
+SPLIT = [(77, 1024), (77, 6144), (150, 6144), (200, 6144), (200, 12288)]
+SPLIT_EXPERTS = [([30, 0, 17, 30], 1024, 0), ([1, 60, 0, 9], 4096, 7), ([97, 0, 30, 20], 4096, 3), ([129, 1, 0, 64], 4096, 6),
+                 ([700, 300, 1, 490], 2048, 9)]
+K = 1216
+
+
+def workspace_slices(rows, w, experts):
+    """Parts of K that the call's workspace has room for (bf16 rows: nothing else is in it)."""
+    from fp4_block_scaled_tensor_amd import experts as E
+    nb = E._linear_workspace(rows, 0, w.fmt, w.block, w.layout, w.g_stripe, w.rows, w.k, experts)
+    return nb // (4 * rows * w.rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,block,layout", [("ue5m3", 16, "1d"), ("e4m3", 16, "2dT"), ("e8m0", 32, "1d")])
+@pytest.mark.parametrize("m,n", SPLIT)
+def test_split_k_in_every_tile_height(m, n, fmt, block, layout, dtype):
+    """Exact on integers (quantum 2^-6, sums below 8 * 12 * 1216 < 2^17): equal to float64 bit for bit."""
+    import fp4_block_scaled_tensor_amd as fp4
+    from test_gpu_experts import gen, random_weight
+    r = gen(m + n)
+    n -= 9 if fmt == "e8m0" else 0                       # rows of y without 16-byte alignment
+    w, _ = random_weight(r, n, K, fmt, block, layout, spread=1)
+    assert workspace_slices(m, w, 0) > 1
+    x = torch.from_numpy(r.integers(-8, 9, (m, K)).astype(np.float32)).to(DT[dtype]).cuda()
+    y = fp4.linear(x, w, out_dtype=torch.float32)
+    assert torch.equal(y.double(), x.double() @ fp4.dequantize(w).double().t().contiguous())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,block,layout", [("ue5m3", 16, "1d"), ("e8m0", 32, "1d")])
+@pytest.mark.parametrize("counts,n,dropped", SPLIT_EXPERTS)
+def test_split_k_over_experts(counts, n, dropped, fmt, block, layout, dtype):
+    import fp4_block_scaled_tensor_amd as fp4
+    from test_gpu_experts import gen, random_weight
+    r = gen(sum(counts) + n)
+    pairs = [random_weight(r, n, K, fmt, block, layout, g=2.0 ** e, spread=1) for e in range(len(counts))]
+    stack = fp4.stack_experts([p[0] for p in pairs])
+    ends = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = int(ends[-1]) + dropped
+    assert workspace_slices(rows, stack, len(counts)) > 1
+    x = torch.from_numpy(r.integers(-8, 9, (rows, K)).astype(np.float32)).to(DT[dtype]).cuda()
+    x[int(ends[-1]):] = float("nan")                     # rows of dropped slots are not used
+    y = fp4.expert_linear(x, stack, torch.from_numpy(ends).cuda(), out_dtype=torch.float32)
+    assert (y[int(ends[-1]):] == 0).all()
+    for e, (_, w64) in enumerate(pairs):
+        a, b = int(ends[e]), int(ends[e + 1])
+        if a < b:
+            want = (x[a:b].double() @ torch.from_numpy(w64.T.copy()).cuda()) * 2.0 ** e
+            assert torch.equal(y[a:b].double(), want), e
