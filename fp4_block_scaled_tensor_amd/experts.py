@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 from dataclasses import dataclass
 
 import torch
@@ -82,11 +83,28 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _ld(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype) -> int:
-    """Checks a device matrix [rows, width] of dtype with unit column stride; its row stride (one
-    row's says nothing and is taken as its width)."""
+def _on_its_device(f):
+    """f with the device of its first tensor made current: the library launches on the current one."""
+    first = next(iter(inspect.signature(f).parameters))
+
+    @functools.wraps(f)
+    def call(*args, **kwargs):
+        t = args[0] if args else kwargs.get(first)
+        device = -1 if t is None else t.get_device()
+        if device < 0 or device == torch.cuda.current_device():   # (f refuses a missing or host tensor)
+            return f(*args, **kwargs)
+        with torch.cuda.device(device):
+            return f(*args, **kwargs)
+    return call
+
+
+def _ld(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype, like: torch.Tensor) -> int:
+    """Checks a matrix [rows, width] of dtype with unit column stride on like's device; its row stride
+    (one row's says nothing and is taken as its width)."""
     if not t.is_cuda:
         _dev_check(t)
+    if t is not like and t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
     shape = t.shape
     if len(shape) != 2 or shape[0] != rows or shape[1] != width:
         raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(shape)}")
@@ -125,7 +143,8 @@ def _sort_workspace(tokens: int, topk: int, n_experts: int) -> int:
 
 @functools.lru_cache(maxsize=4096)
 def _linear_workspace(rows: int, dtype: int, fmt: int, block: int, layout: int, g_stripe: int, n: int, k: int,
-                      n_experts: int) -> int:
+                      n_experts: int, device: int = -1) -> int:
+    """(device, the current one, is here for what is remembered: its compute units decide how K is split.)"""
     ws = ctypes.c_size_t()
     op = _lib.Operand(None, None, None, fmt, block, layout, g_stripe, n, k)
     _lib.check(_lib.load().fp4_linear_workspace(rows, dtype, ctypes.byref(op), n_experts, ctypes.byref(ws)))
@@ -139,6 +158,7 @@ def _address(workspace: torch.Tensor | None) -> int | None:
     return None if workspace is None else workspace.data_ptr()
 
 
+@_on_its_device
 def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
     """fp4_expert_sort: the plan of ids [tokens, topk] (int32 or int64; an id outside
     [0, n_experts) drops its slot)."""
@@ -147,7 +167,7 @@ def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
         raise ValueError("ids must be a 2-D int32 or int64 tensor")
     topk = _width("ids", ids)
     tokens = ids.shape[0]
-    ld = _ld("ids", ids, tokens, topk, ids.dtype)
+    ld = _ld("ids", ids, tokens, topk, ids.dtype, ids)
     n, dev = tokens * topk, ids.device
     nb = _sort_workspace(tokens, topk, n_experts)
     order = torch.empty(n, dtype=torch.int32, device=dev)
@@ -160,63 +180,67 @@ def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
     return ExpertPlan(order, pos, offsets, tokens, topk, n_experts)
 
 
+@_on_its_device
 def expert_gather(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_gather: token rows [tokens, hidden] in expert order, [tokens * topk, hidden];
     dropped slots give zero rows."""
     lib = _lib.load()
     h, n = _width("x", x), plan.tokens * plan.topk
-    ldx = _ld("x", x, plan.tokens, h, x.dtype)
+    ldx = _ld("x", x, plan.tokens, h, x.dtype, x)
     dt = _dtype(x, "x")
     if out is None:
         out, ldo = x.new_empty((n, h)), h
     else:
-        ldo = _ld("out", out, n, h, x.dtype)
+        ldo = _ld("out", out, n, h, x.dtype, x)
     _lib.check(lib.fp4_expert_gather(x.data_ptr(), dt, plan.tokens, h, ldx, _pos(plan, x), plan.topk,
                                      out.data_ptr(), ldo, _stream_of(x)))
     return out
 
 
+@_on_its_device
 def expert_gather_grad(dxs: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_gather_grad: each token's sum [tokens, hidden] of its kept slots' rows."""
     lib = _lib.load()
     h = _width("dxs", dxs)
-    ld = _ld("dxs", dxs, plan.tokens * plan.topk, h, dxs.dtype)
+    ld = _ld("dxs", dxs, plan.tokens * plan.topk, h, dxs.dtype, dxs)
     dt = _dtype(dxs, "dxs")
     if out is None:
         out, ldo = dxs.new_empty((plan.tokens, h)), h
     else:
-        ldo = _ld("out", out, plan.tokens, h, dxs.dtype)
+        ldo = _ld("out", out, plan.tokens, h, dxs.dtype, dxs)
     _lib.check(lib.fp4_expert_gather_grad(dxs.data_ptr(), dt, plan.tokens, h, ld, _pos(plan, dxs), plan.topk,
                                           out.data_ptr(), ldo, _stream_of(dxs)))
     return out
 
 
+@_on_its_device
 def expert_combine(ys: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_combine: each token's weighted sum [tokens, hidden] of its kept slots' rows ys
     [tokens * topk, hidden]; weights float32 [tokens, topk]."""
     lib = _lib.load()
     h = _width("ys", ys)
-    ld = _ld("ys", ys, plan.tokens * plan.topk, h, ys.dtype)
-    ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32)
+    ld = _ld("ys", ys, plan.tokens * plan.topk, h, ys.dtype, ys)
+    ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32, ys)
     dt = _dtype(ys, "ys")
     if out is None:
         out, ldo = ys.new_empty((plan.tokens, h)), h
     else:
-        ldo = _ld("out", out, plan.tokens, h, ys.dtype)
+        ldo = _ld("out", out, plan.tokens, h, ys.dtype, ys)
     _lib.check(lib.fp4_expert_combine(ys.data_ptr(), dt, plan.tokens, h, ld, weights.data_ptr(), ldw,
                                       _pos(plan, ys), plan.topk, out.data_ptr(), ldo, _stream_of(ys)))
     return out
 
 
+@_on_its_device
 def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan):
     """fp4_expert_combine_grad: (dys [tokens * topk, hidden] of ys's dtype, dweights float32
     [tokens, topk]) for dy [tokens, hidden]."""
     lib = _lib.load()
     h, n = _width("dy", dy), plan.tokens * plan.topk
-    lddy = _ld("dy", dy, plan.tokens, h, dy.dtype)
-    ldys = _ld("ys", ys, n, h, dy.dtype)
-    ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32)
+    lddy = _ld("dy", dy, plan.tokens, h, dy.dtype, dy)
+    ldys = _ld("ys", ys, n, h, dy.dtype, dy)
+    ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32, dy)
     dt = _dtype(dy, "dy")
     dys = dy.new_empty((n, h))
     dw = weights.new_empty((plan.tokens, plan.topk))
@@ -228,19 +252,20 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
 
 def _product(x, w, rows, n_experts, out_dtype, out):
     """What linear and expert_linear share: checks, output, workspace (a tensor to hold, see _address)."""
-    ldx = _ld("x", x, rows, w.k, x.dtype)
+    ldx = _ld("x", x, rows, w.k, x.dtype, x)
     dt = _dtype(x, "x")
     if out is None:
         out = x.new_empty((rows, w.rows)) if out_dtype is None else x.new_empty((rows, w.rows), dtype=out_dtype)
         ldo = w.rows
     else:
-        ldo = _ld("out", out, rows, w.rows, out_dtype or out.dtype)
+        ldo = _ld("out", out, rows, w.rows, out_dtype or out.dtype, x)
     odt = _dtype(out, "out")
-    nb = _linear_workspace(rows, dt, w.fmt, w.block, w.layout, w.g_stripe, w.rows, w.k, n_experts)
+    nb = _linear_workspace(rows, dt, w.fmt, w.block, w.layout, w.g_stripe, w.rows, w.k, n_experts, x.get_device())
     ws = x.new_empty(nb, dtype=torch.uint8) if nb else None
     return ldx, dt, out, ldo, odt, ws, nb
 
 
+@_on_its_device
 def linear(x: torch.Tensor, w: QTensor, out_dtype=None, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_linear: x [rows, k] (bf16 or float32, not quantized) times the FP4 weight w [n, k]
     transposed, [rows, n] in out_dtype (x's by default). The transposed operand of a TILE2D weight
@@ -256,6 +281,7 @@ def linear(x: torch.Tensor, w: QTensor, out_dtype=None, out: torch.Tensor | None
     return out
 
 
+@_on_its_device
 def expert_linear(x: torch.Tensor, w: ExpertWeights, plan: ExpertPlan | torch.Tensor, out_dtype=None,
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_linear: rows x [rows, k] in expert order, each times its expert's weight

@@ -139,3 +139,75 @@ def test_expert_linear_checks_the_offsets(offsets, record):
     with pytest.raises(ValueError, match="offsets"):
         fp4.expert_linear(torch.zeros((8, 128), dtype=torch.bfloat16), weight(32, 128, 3), offsets)
     assert not names
+
+
+# ------------------------------------------------------------------ devices
+
+class On:
+    """Stands for a tensor of CUDA device `index`."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+
+def test_calls_run_with_their_tensors_device_current(monkeypatch):
+    """The library launches on the current device, so the first tensor's is made current around the call."""
+    now = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+
+    @experts._on_its_device
+    def call(x, factor=1):
+        """doc"""
+        if factor < 0:
+            raise ValueError("refused")
+        return now[0], x.index * factor
+    assert call(On(0)) == (0, 0) and call(On(2)) == (2, 2) and call(x=On(3), factor=2) == (3, 6)
+    with pytest.raises(ValueError, match="refused"):
+        call(On(1), -1)
+    assert now == [0] and call.__doc__ == "doc"
+    assert call(On(-1)) == (0, -1)          # a host tensor: the call itself refuses it
+
+
+@pytest.mark.parametrize("name", ["expert_sort", "expert_gather", "expert_gather_grad", "expert_combine",
+                                  "expert_combine_grad", "linear", "expert_linear"])
+def test_every_entry_point_makes_its_device_current(name):
+    assert getattr(fp4, name).__wrapped__.__name__ == name
+
+
+def on_meta(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype, device="meta")
+
+
+ELSEWHERE = {
+    "gather_out": lambda: fp4.expert_gather(torch.zeros(4, 8), plan_of(), out=on_meta(8, 8)),
+    "gather_grad_out": lambda: fp4.expert_gather_grad(torch.zeros(8, 8), plan_of(), out=on_meta(4, 8)),
+    "combine_weights": lambda: fp4.expert_combine(torch.zeros(8, 8), on_meta(4, 2), plan_of()),
+    "combine_out": lambda: fp4.expert_combine(torch.zeros(8, 8), torch.zeros(4, 2), plan_of(), out=on_meta(4, 8)),
+    "grad_ys": lambda: fp4.expert_combine_grad(torch.zeros(4, 8), on_meta(8, 8), torch.zeros(4, 2), plan_of()),
+    "grad_weights": lambda: fp4.expert_combine_grad(torch.zeros(4, 8), torch.zeros(8, 8), on_meta(4, 2), plan_of()),
+    "linear_out": lambda: fp4.linear(torch.zeros(4, 128), weight(32, 128), out=on_meta(4, 32)),
+    "experts_out": lambda: fp4.expert_linear(torch.zeros(8, 128), weight(32, 128, 3), plan_of(), out=on_meta(8, 32)),
+}
+
+
+@pytest.mark.parametrize("case", ELSEWHERE)
+def test_tensors_of_one_call_share_a_device(case, record):
+    names = []
+    record(lambda name, args: names.append(name))
+    with pytest.raises(ValueError, match="must be on cpu"):
+        ELSEWHERE[case]()
+    assert not names
