@@ -105,9 +105,8 @@ def _ld(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype, l
         _dev_check(t)
     if t is not like and t.device != like.device:
         raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != width:
-        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(shape)}")
+    if t.shape != (rows, width):
+        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     stride = t.stride()
@@ -127,11 +126,11 @@ def _pos(plan: ExpertPlan, like: torch.Tensor) -> int:
     return pos.data_ptr()
 
 
-def _width(name: str, t: torch.Tensor) -> int:
+def _sizes(name: str, t: torch.Tensor) -> tuple[int, int]:
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
-    return shape[1]
+    return shape
 
 
 @functools.lru_cache(maxsize=4096)
@@ -165,13 +164,12 @@ def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
     lib = _lib.load()
     if ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("ids must be a 2-D int32 or int64 tensor")
-    topk = _width("ids", ids)
-    tokens = ids.shape[0]
+    tokens, topk = _sizes("ids", ids)
     ld = _ld("ids", ids, tokens, topk, ids.dtype, ids)
     n, dev = tokens * topk, ids.device
     nb = _sort_workspace(tokens, topk, n_experts)
     order = torch.empty(n, dtype=torch.int32, device=dev)
-    pos = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    pos = torch.empty(tokens, topk, dtype=torch.int32, device=dev)
     offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
     work = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
     _lib.check(lib.fp4_expert_sort(ids.data_ptr(), int(ids.dtype is torch.int64), tokens, topk, ld, n_experts,
@@ -185,11 +183,11 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = 
     """fp4_expert_gather: token rows [tokens, hidden] in expert order, [tokens * topk, hidden];
     dropped slots give zero rows."""
     lib = _lib.load()
-    h, n = _width("x", x), plan.tokens * plan.topk
+    (_, h), n = _sizes("x", x), plan.tokens * plan.topk
     ldx = _ld("x", x, plan.tokens, h, x.dtype, x)
     dt = _dtype(x, "x")
     if out is None:
-        out, ldo = x.new_empty((n, h)), h
+        out, ldo = x.new_empty(n, h), h
     else:
         ldo = _ld("out", out, n, h, x.dtype, x)
     _lib.check(lib.fp4_expert_gather(x.data_ptr(), dt, plan.tokens, h, ldx, _pos(plan, x), plan.topk,
@@ -201,11 +199,11 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = 
 def expert_gather_grad(dxs: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_gather_grad: each token's sum [tokens, hidden] of its kept slots' rows."""
     lib = _lib.load()
-    h = _width("dxs", dxs)
+    _, h = _sizes("dxs", dxs)
     ld = _ld("dxs", dxs, plan.tokens * plan.topk, h, dxs.dtype, dxs)
     dt = _dtype(dxs, "dxs")
     if out is None:
-        out, ldo = dxs.new_empty((plan.tokens, h)), h
+        out, ldo = dxs.new_empty(plan.tokens, h), h
     else:
         ldo = _ld("out", out, plan.tokens, h, dxs.dtype, dxs)
     _lib.check(lib.fp4_expert_gather_grad(dxs.data_ptr(), dt, plan.tokens, h, ld, _pos(plan, dxs), plan.topk,
@@ -219,12 +217,12 @@ def expert_combine(ys: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     """fp4_expert_combine: each token's weighted sum [tokens, hidden] of its kept slots' rows ys
     [tokens * topk, hidden]; weights float32 [tokens, topk]."""
     lib = _lib.load()
-    h = _width("ys", ys)
+    _, h = _sizes("ys", ys)
     ld = _ld("ys", ys, plan.tokens * plan.topk, h, ys.dtype, ys)
     ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32, ys)
     dt = _dtype(ys, "ys")
     if out is None:
-        out, ldo = ys.new_empty((plan.tokens, h)), h
+        out, ldo = ys.new_empty(plan.tokens, h), h
     else:
         ldo = _ld("out", out, plan.tokens, h, ys.dtype, ys)
     _lib.check(lib.fp4_expert_combine(ys.data_ptr(), dt, plan.tokens, h, ld, weights.data_ptr(), ldw,
@@ -237,17 +235,44 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
     """fp4_expert_combine_grad: (dys [tokens * topk, hidden] of ys's dtype, dweights float32
     [tokens, topk]) for dy [tokens, hidden]."""
     lib = _lib.load()
-    h, n = _width("dy", dy), plan.tokens * plan.topk
+    (_, h), n = _sizes("dy", dy), plan.tokens * plan.topk
     lddy = _ld("dy", dy, plan.tokens, h, dy.dtype, dy)
     ldys = _ld("ys", ys, n, h, dy.dtype, dy)
     ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32, dy)
     dt = _dtype(dy, "dy")
-    dys = dy.new_empty((n, h))
-    dw = weights.new_empty((plan.tokens, plan.topk))
+    dys = dy.new_empty(n, h)
+    dw = weights.new_empty(plan.tokens, plan.topk)
     _lib.check(lib.fp4_expert_combine_grad(dy.data_ptr(), dt, plan.tokens, h, lddy, ys.data_ptr(), ldys,
                                            weights.data_ptr(), ldw, _pos(plan, dy), plan.topk, dys.data_ptr(), h,
                                            dw.data_ptr(), plan.topk, _stream_of(dy)))
     return dys, dw
+
+
+@functools.lru_cache(maxsize=4096)
+def _weight_bytes(rows: int, k: int, block: int, layout: int, g_stripe: int) -> tuple[int, int, int]:
+    """Bytes of one weight's payload, scale codes and g."""
+    scales = rows * (k // block) if layout == _lib.FP4_SCALES_1D else (rows // 16) * (k // 16)
+    return rows * (k // 2), scales, 4 * max(1, -(-rows // g_stripe) if g_stripe else 1)
+
+
+def _check_weight(w: QTensor | ExpertWeights, n_experts: int, like: torch.Tensor) -> None:
+    """The buffers of a weight (n_experts 0) or of a stack against its sizes: packed on like's device, and
+    a stack's experts without a gap."""
+    q, s, g, dev, many = w.q, w.s, w.g, like.device, n_experts or 1
+    nq, ns, ng = _weight_bytes(w.rows, w.k, w.block, w.layout, w.g_stripe)
+    if not ((q.nbytes == nq * many or (q.nbytes > nq and not n_experts)) and q.is_contiguous() and q.device == dev
+            and q.element_size() == 1):
+        bad, t, size = "payload", q, nq
+    elif not ((s.nbytes == ns * many or (s.nbytes > ns and not n_experts)) and s.is_contiguous() and s.device == dev
+              and s.element_size() == 1):
+        bad, t, size = "scales", s, ns
+    elif not ((g.nbytes == ng * many or (g.nbytes > ng and not n_experts) or (g.nbytes == 0 and not w.g_stripe))   # none: 1
+              and g.is_contiguous() and g.device == dev and g.dtype is torch.float32):
+        bad, t, size = "g", g, ng
+    else:
+        return
+    raise ValueError(f"the weight's {bad} must be a contiguous {'float32' if t is g else 'uint8'} tensor of "
+                     f"{size * many} bytes on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _product(x, w, rows, n_experts, out_dtype, out):
@@ -255,12 +280,13 @@ def _product(x, w, rows, n_experts, out_dtype, out):
     ldx = _ld("x", x, rows, w.k, x.dtype, x)
     dt = _dtype(x, "x")
     if out is None:
-        out = x.new_empty((rows, w.rows)) if out_dtype is None else x.new_empty((rows, w.rows), dtype=out_dtype)
+        out = x.new_empty(rows, w.rows) if out_dtype is None else x.new_empty((rows, w.rows), dtype=out_dtype)
         ldo = w.rows
     else:
         ldo = _ld("out", out, rows, w.rows, out_dtype or out.dtype, x)
     odt = _dtype(out, "out")
     nb = _linear_workspace(rows, dt, w.fmt, w.block, w.layout, w.g_stripe, w.rows, w.k, n_experts, x.get_device())
+    _check_weight(w, n_experts, x)
     ws = x.new_empty(nb, dtype=torch.uint8) if nb else None
     return ldx, dt, out, ldo, odt, ws, nb
 
@@ -271,10 +297,8 @@ def linear(x: torch.Tensor, w: QTensor, out_dtype=None, out: torch.Tensor | None
     transposed, [rows, n] in out_dtype (x's by default). The transposed operand of a TILE2D weight
     gives the gradient dX = dY . W."""
     lib = _lib.load()
-    _width("x", x)
-    rows = x.shape[0]
+    rows, _ = _sizes("x", x)
     ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, 0, out_dtype, out)
-    _dev_check(w.q)
     op = w.operand()
     _lib.check(lib.fp4_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), out.data_ptr(), odt, ldo, _address(ws),
                               nb, _stream_of(x)))
@@ -291,15 +315,13 @@ def expert_linear(x: torch.Tensor, w: ExpertWeights, plan: ExpertPlan | torch.Te
     lib = _lib.load()
     offsets = plan.offsets if isinstance(plan, ExpertPlan) else plan
     experts = w.n_experts
-    _width("x", x)
-    rows = x.shape[0]
+    rows, _ = _sizes("x", x)
     if (offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous()
             or offsets.device != x.device):
         raise ValueError(f"offsets must be a contiguous int32 tensor of {experts + 1} elements on {x.device}")
     if isinstance(plan, ExpertPlan) and rows != plan.tokens * plan.topk:
         raise ValueError(f"x must have the plan's {plan.tokens * plan.topk} rows (tokens * topk), got {rows}")
     ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, experts, out_dtype, out)
-    _dev_check(w.q)
     op = w.operand()
     _lib.check(lib.fp4_expert_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), experts, offsets.data_ptr(),
                                      out.data_ptr(), odt, ldo, _address(ws), nb, _stream_of(x)))

@@ -211,3 +211,71 @@ def test_tensors_of_one_call_share_a_device(case, record):
     with pytest.raises(ValueError, match="must be on cpu"):
         ELSEWHERE[case]()
     assert not names
+
+
+# ------------------------------------------------------------------ weights
+
+def replaced(w, **changes):
+    import dataclasses
+    return dataclasses.replace(w, **changes)
+
+
+BAD_WEIGHTS = {
+    "payload_type": lambda w: replaced(w, q=w.q.to(torch.int32)),
+    "payload_short": lambda w: replaced(w, q=w.q[..., :-1, :].contiguous()),
+    "payload_strided": lambda w: replaced(w, q=torch.zeros((*w.q.shape[:-1], 2 * w.q.shape[-1]), dtype=torch.uint8)[..., ::2]),
+    "payload_elsewhere": lambda w: replaced(w, q=w.q.to("meta")),
+    "scales_type": lambda w: replaced(w, s=w.s.to(torch.int32)),
+    "scales_short": lambda w: replaced(w, s=w.s[..., :-1].contiguous()),
+    "scales_strided": lambda w: replaced(w, s=w.s.transpose(-1, -2)),
+    "scales_elsewhere": lambda w: replaced(w, s=w.s.to("meta")),
+    "g_type": lambda w: replaced(w, g=w.g.double()),
+    "g_short": lambda w: replaced(w, g=w.g[..., :-1].contiguous()),
+    "g_elsewhere": lambda w: replaced(w, g=w.g.to("meta")),
+}
+
+
+def ue5m3_weight(n, k, count=None, layout=None, stripe=32):
+    layout = fp4.FP4_SCALES_1D if layout is None else layout
+    if count is not None:
+        return fp4.stack_experts([ue5m3_weight(n, k, None, layout, stripe) for _ in range(count)])
+    shape = {fp4.FP4_SCALES_1D: (n, k // 16), fp4.FP4_SCALES_2D: (n // 16, k // 16),
+             fp4.FP4_SCALES_2D_T: (k // 16, n // 16)}[layout]
+    return fp4.QTensor(torch.zeros((n, k // 2), dtype=torch.uint8), torch.zeros(shape, dtype=torch.uint8),
+                       torch.ones(-(-n // stripe) if stripe else 1), fp4.UE5M3, 16, layout, n, k, stripe)
+
+
+@pytest.mark.parametrize("bad", BAD_WEIGHTS)
+@pytest.mark.parametrize("count", [None, 3])
+def test_products_check_the_weights_buffers(bad, count, record):
+    """QTensor and ExpertWeights are built by callers, too: the kernels read their buffers as packed codes of the
+    sizes that rows, k, block, layout and g_stripe say."""
+    names = []
+    record(lambda name, args: names.append(name))
+    x = torch.zeros((8, 128), dtype=torch.bfloat16)
+
+    def call(w):
+        return fp4.linear(x, w) if count is None else fp4.expert_linear(x, w, plan_of())
+    w = ue5m3_weight(80, 128, count)
+    call(w)
+    assert len(names) == 1
+    with pytest.raises(ValueError, match="payload|scales|g "):
+        call(BAD_WEIGHTS[bad](w))
+    assert len(names) == 1
+
+
+@pytest.mark.parametrize("count", [None, 3])
+def test_every_form_of_a_weight_is_taken(count, record):
+    names = []
+    record(lambda name, args: names.append(name))
+    x = torch.zeros((8, 128), dtype=torch.bfloat16)
+    weights = [weight(37, 128, count), ue5m3_weight(37, 128, count, stripe=0), ue5m3_weight(37, 128, count, stripe=16),
+               ue5m3_weight(48, 128, count, fp4.FP4_SCALES_2D, 0), ue5m3_weight(48, 128, count, fp4.FP4_SCALES_2D_T, 0),
+               weight(0, 128, count)]
+    weights.append(replaced(weights[1], g=weights[1].g[..., :0]))     # no tensor scale: 1
+    for w in weights:
+        fp4.linear(x, w) if count is None else fp4.expert_linear(x, w, plan_of())
+    assert len(names) == len(weights)
+    if count:
+        with pytest.raises(ValueError, match="payload"):             # an expert's codes must follow each other
+            fp4.expert_linear(x, replaced(weights[0], q=torch.zeros((3, 40, 64), dtype=torch.uint8)), plan_of())
