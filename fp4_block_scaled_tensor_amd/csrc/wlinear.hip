@@ -3,8 +3,9 @@
 //
 // E2M1 times a block scale has at most 6 significant bits and lies in bfloat16's range, so the
 // weight decodes to bf16 without rounding and the products run on the bf16 matrix cores with
-// float32 accumulation. A float32 activation is split exactly into three bf16 parts (8 + 8 + 8
-// significant bits by truncation), each multiplied into the same sums.
+// float32 accumulation. (E8M0 codes 253 and 254 reach past that range, which is float32's, with the
+// larger E2M1 values, and those weights are infinite.) A float32 activation is split into three bf16
+// parts (8 + 8 + 8 significant bits by truncation), each multiplied into the same sums.
 #include "experts.hpp"
 
 namespace fp4k {
@@ -89,9 +90,9 @@ __device__ __forceinline__ v8bf decode8_bf16(uint32_t w, float sv) {
   return __builtin_bit_cast(v8bf, r);
 }
 
-// 8 float32 -> three bf16 vectors whose exact sum they are. Each part keeps the upper 16 bits
-// of what is left (truncation, so no part overflows); an infinity has no remainder and a NaN's
-// remainder is NaN.
+// 8 float32 -> three bf16 vectors whose sum they are, exactly from magnitude 2^-110 on (the last part
+// holds no bits below 2^-133). Each part keeps the upper 16 bits of what is left (truncation, so no
+// part overflows); an infinity has no remainder and a NaN's remainder is NaN.
 __device__ __forceinline__ void split3(const float* v, v8bf* part) {
   float r[8];
 #pragma unroll
@@ -733,7 +734,7 @@ __global__ __launch_bounds__(256) void k_join_slices(const float* __restrict__ p
   }
 }
 
-// float32 rows -> three planes of bf16 rows whose exact sum they are
+// float32 rows -> three planes of bf16 rows whose sum they are (split3)
 __global__ __launch_bounds__(256) void k_split3(const float* __restrict__ x, int64_t ldx, int64_t rows, int64_t K,
                                                 char* __restrict__ out) {
   const int64_t per = K / 8, n = rows * per, plane = rows * K * 2;

@@ -85,10 +85,14 @@ fp4_status fp4_expert_combine_grad(const void* dy, int32_t dtype, int64_t tokens
  *   y        device, [rows x N] of y_dtype, row stride ldy elements (>= N; element aligned)
  *   ws       device workspace of at least the bytes fp4_linear_workspace gives (16-byte aligned;
  *            may be NULL when that is 0)
- * Arithmetic: E2M1 * S is exact in bfloat16. bf16 x: bf16 matrix products accumulated in float32.
- * float32 x: each element is split exactly into three bf16 parts, whose products accumulate in
- * the same float32 sums. The sum is multiplied by g in float32 and rounded once to y_dtype. The
- * order of the sums depends on the sizes only: equal calls give equal bits. K = 0 gives zeros.
+ * Arithmetic: E2M1 * S is exact in bfloat16. (E8M0 codes 253 and 254, which fp4_quantize writes for no
+ * finite weight, make products from 2^128 on: they are infinite, as in float32.) bf16 x: bf16 matrix
+ * products accumulated in float32. float32 x: each element is split into three bf16 parts, whose
+ * products accumulate in the same float32 sums; the parts add up to x exactly from magnitude 2^-110
+ * on, below it bits under 2^-133 (bfloat16's least subnormal) are dropped; an infinite product with
+ * a weight that is itself infinite is NaN. The sum, over all of K, is multiplied by g in float32 and
+ * rounded once to y_dtype. The order of the sums depends on the sizes and the device only: equal
+ * calls give equal bits. K = 0 gives zeros.
  *
  * fp4_expert_linear - rows in expert order: row p with offsets[e] <= p < offsets[e+1] uses
  * expert e's weight; rows from offsets[n_experts] on are written as zeros.
