@@ -1,4 +1,6 @@
-"""Edges of the mixture-of-experts operators: no tokens with any number of experts."""
+"""Edges of the mixture-of-experts operators: no tokens with any number of experts, every bit pattern of a
+gathered row."""
+import numpy as np
 import pytest
 import torch
 
@@ -18,3 +20,29 @@ def test_sort_without_tokens_writes_the_offsets(experts, ids64):
     assert offsets.cpu().tolist() == [0] * (experts + 1) + [-7] * 8
     plan = fp4.expert_sort(torch.empty((0, 2), dtype=torch.int32, device="cuda"), experts)
     assert plan.offsets.cpu().tolist() == [0] * (experts + 1) and plan.pos.shape == (0, 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hidden,pad", [(4096, 0), (4093, 3), (7, 0)])
+def test_gather_copies_bits(hidden, pad, dtype):
+    """A gathered row is its token's row bit for bit: subnormals, signed zeros, and NaNs with their payloads."""
+    import fp4_block_scaled_tensor_amd as fp4
+    r = np.random.Generator(np.random.PCG64(hidden))
+    tokens, topk, experts = 33, 3, 4
+    if dtype == "bf16":
+        bits = (np.arange(tokens * hidden, dtype=np.int64) * 40503 % 65536).astype(np.uint16).view(np.int16).reshape(tokens, hidden)
+        kind = torch.bfloat16
+    else:
+        bits = r.integers(0, 2 ** 32, (tokens, hidden), dtype=np.uint32)
+        nan = r.random((tokens, hidden)) < 0.2
+        bits = np.where(nan, bits | np.uint32(0x7F800000), bits).astype(np.uint32).view(np.int32)
+        kind = torch.float32
+    x = torch.zeros((tokens, hidden + pad), dtype=torch.from_numpy(bits).dtype, device="cuda")
+    x[:, :hidden] = torch.from_numpy(bits).cuda()
+    ids = torch.from_numpy(r.integers(-1, experts, (tokens, topk)).astype(np.int32)).cuda()
+    plan = fp4.expert_sort(ids, experts)
+    xs = fp4.expert_gather(x.view(kind)[:, :hidden], plan)
+    order, kept = plan.order.cpu().numpy(), int(plan.offsets[-1])
+    want = np.zeros((tokens * topk, hidden), bits.dtype)
+    want[:kept] = bits[order[:kept] // topk]
+    assert np.array_equal(xs.view(x.dtype).cpu().numpy(), want)
