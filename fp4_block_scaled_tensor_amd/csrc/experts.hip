@@ -179,7 +179,7 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_count(const void* __re
   const int keys = E + 1;
   constexpr int NK = SORT_WAVE_SLOTS / 64;
   const int lo = min(n, (int)((blockIdx.x * SORT_WAVES + (threadIdx.x >> 6)) * SORT_WAVE_SLOTS));
-  const int hi = min(n, lo + SORT_WAVE_SLOTS);
+  const int hi = lo + min(n - lo, SORT_WAVE_SLOTS);   // (lo + SORT_WAVE_SLOTS can pass 2^31)
   uint32_t key[NK];
   wave_keys<ID64, NK>(ids, ld, topk, E, lo, hi, key);
   for (int i = threadIdx.x; i < keys; i += SORT_WAVES * 64) rows[i] = 0;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(SORT_WAVES * 64) void k_sort_place(const void* __re
   int* before = lds + keys;
   int* rows = lds + 2 * keys;
   constexpr int NK = SORT_WAVE_SLOTS / 64;
-  const int lo = min(n, (chunk * SORT_WAVES + w) * SORT_WAVE_SLOTS), hi = min(n, lo + SORT_WAVE_SLOTS);
+  const int lo = min(n, (chunk * SORT_WAVES + w) * SORT_WAVE_SLOTS), hi = lo + min(n - lo, SORT_WAVE_SLOTS);
   uint32_t key[NK];
   wave_keys<ID64, NK>(ids, ld, topk, E, lo, hi, key);
   for (int i = threadIdx.x; i < (2 + SORT_WAVES) * keys; i += NTH) lds[i] = 0;

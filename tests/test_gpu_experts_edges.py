@@ -46,3 +46,26 @@ def test_gather_copies_bits(hidden, pad, dtype):
     want = np.zeros((tokens * topk, hidden), bits.dtype)
     want[:kept] = bits[order[:kept] // topk]
     assert np.array_equal(xs.view(x.dtype).cpu().numpy(), want)
+
+
+def test_sort_of_almost_2_to_the_31_slots():
+    """The largest number of slots: the last wave's range ends at 2^31 - 1. All slots of expert 0 but the first, the
+    middle one and the last (expert 1), so every position is known."""
+    import fp4_block_scaled_tensor_amd as fp4
+    n = 2 ** 31 - 1
+    mid = n // 2
+    ids = torch.zeros((n, 1), dtype=torch.int32, device="cuda")
+    for s in (0, mid, n - 1):
+        ids[s] = 1
+    plan = fp4.expert_sort(ids, 2)
+    assert plan.offsets.cpu().tolist() == [0, n - 3, n]
+    order, pos = plan.order, plan.pos.view(-1)
+    assert order[-3:].cpu().tolist() == [0, mid, n - 1]
+    assert pos[0] == n - 3 and pos[mid] == n - 2 and pos[n - 1] == n - 1
+    step = 2 ** 27
+    for lo in range(0, n - 3, step):                      # position p holds slot p + 1, from the middle on p + 2
+        hi = min(lo + step, n - 3)
+        p = torch.arange(lo, hi, device="cuda")
+        slot = p + 1 + (p + 1 >= mid)
+        assert torch.equal(order[lo:hi].long(), slot), lo
+        assert torch.equal(pos[slot].long(), p), lo
