@@ -67,12 +67,13 @@ def stack_experts(weights: list[QTensor]) -> ExpertWeights:
 # workspace sizes, which depend on nothing but the sizes, are remembered by them.
 _DTYPES = {torch.bfloat16: _lib.FP4_IN_BF16, torch.float32: _lib.FP4_IN_FP32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_of(t: torch.Tensor) -> int:
     """The current stream of t's device."""
     if _raw_stream is not None:
-        return _raw_stream(t.device.index)
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -91,28 +92,41 @@ def _on_its_device(f):
     def call(*args, **kwargs):
         t = args[0] if args else kwargs.get(first)
         device = -1 if t is None else t.get_device()
-        if device < 0 or device == torch.cuda.current_device():   # (f refuses a missing or host tensor)
+        if device < 0 or device == _current_device():   # (f refuses a missing or host tensor)
             return f(*args, **kwargs)
         with torch.cuda.device(device):
             return f(*args, **kwargs)
     return call
 
 
-def _ld(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype, like: torch.Tensor) -> int:
-    """Checks a matrix [rows, width] of dtype with unit column stride on like's device; its row stride
-    (one row's says nothing and is taken as its width)."""
+def _matrix(name: str, t: torch.Tensor) -> tuple[int, int, int]:
+    """Checks a device matrix with unit column stride, a call's first; its rows, width and row stride (one
+    row's says nothing and is taken as its width)."""
     if not t.is_cuda:
         _dev_check(t)
-    if t is not like and t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    if t.shape != (rows, width):
-        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    stride = t.stride()
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
+    rows, width = shape
     if width > 1 and stride[1] != 1:
         raise ValueError(f"{name} must have unit column stride")
-    return stride[0] if rows > 1 else width
+    return rows, width, stride[0] if rows > 1 else width
+
+
+def _ld(name: str, t: torch.Tensor, rows: int, width: int, dtype: torch.dtype, like: torch.Tensor) -> int:
+    """Checks a further matrix of a call, [rows, width] of dtype on the device of its first; its row stride."""
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    got, wide, ld = _matrix(name, t)
+    if got != rows or wide != width:
+        raise _mismatch(name, t, rows, width)
+    return ld
+
+
+def _mismatch(name: str, t: torch.Tensor, rows: int, width: int) -> ValueError:
+    return ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
 
 
 def _pos(plan: ExpertPlan, like: torch.Tensor) -> int:
@@ -124,13 +138,6 @@ def _pos(plan: ExpertPlan, like: torch.Tensor) -> int:
         raise ValueError(f"plan.pos must be a contiguous int32 tensor [{plan.tokens}, {plan.topk}] on {like.device}, got "
                          f"{pos.dtype} {tuple(pos.shape)} on {pos.device}")
     return pos.data_ptr()
-
-
-def _sizes(name: str, t: torch.Tensor) -> tuple[int, int]:
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
-    return shape
 
 
 @functools.lru_cache(maxsize=4096)
@@ -164,8 +171,7 @@ def expert_sort(ids: torch.Tensor, n_experts: int) -> ExpertPlan:
     lib = _lib.load()
     if ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("ids must be a 2-D int32 or int64 tensor")
-    tokens, topk = _sizes("ids", ids)
-    ld = _ld("ids", ids, tokens, topk, ids.dtype, ids)
+    tokens, topk, ld = _matrix("ids", ids)
     n, dev = tokens * topk, ids.device
     nb = _sort_workspace(tokens, topk, n_experts)
     order = torch.empty(n, dtype=torch.int32, device=dev)
@@ -183,8 +189,9 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = 
     """fp4_expert_gather: token rows [tokens, hidden] in expert order, [tokens * topk, hidden];
     dropped slots give zero rows."""
     lib = _lib.load()
-    (_, h), n = _sizes("x", x), plan.tokens * plan.topk
-    ldx = _ld("x", x, plan.tokens, h, x.dtype, x)
+    (rows, h, ldx), n = _matrix("x", x), plan.tokens * plan.topk
+    if rows != plan.tokens:
+        raise _mismatch("x", x, plan.tokens, h)
     dt = _dtype(x, "x")
     if out is None:
         out, ldo = x.new_empty(n, h), h
@@ -199,8 +206,9 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = 
 def expert_gather_grad(dxs: torch.Tensor, plan: ExpertPlan, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp4_expert_gather_grad: each token's sum [tokens, hidden] of its kept slots' rows."""
     lib = _lib.load()
-    _, h = _sizes("dxs", dxs)
-    ld = _ld("dxs", dxs, plan.tokens * plan.topk, h, dxs.dtype, dxs)
+    rows, h, ld = _matrix("dxs", dxs)
+    if rows != plan.tokens * plan.topk:
+        raise _mismatch("dxs", dxs, plan.tokens * plan.topk, h)
     dt = _dtype(dxs, "dxs")
     if out is None:
         out, ldo = dxs.new_empty(plan.tokens, h), h
@@ -217,8 +225,9 @@ def expert_combine(ys: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan,
     """fp4_expert_combine: each token's weighted sum [tokens, hidden] of its kept slots' rows ys
     [tokens * topk, hidden]; weights float32 [tokens, topk]."""
     lib = _lib.load()
-    _, h = _sizes("ys", ys)
-    ld = _ld("ys", ys, plan.tokens * plan.topk, h, ys.dtype, ys)
+    rows, h, ld = _matrix("ys", ys)
+    if rows != plan.tokens * plan.topk:
+        raise _mismatch("ys", ys, plan.tokens * plan.topk, h)
     ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32, ys)
     dt = _dtype(ys, "ys")
     if out is None:
@@ -235,8 +244,9 @@ def expert_combine_grad(dy: torch.Tensor, ys: torch.Tensor, weights: torch.Tenso
     """fp4_expert_combine_grad: (dys [tokens * topk, hidden] of ys's dtype, dweights float32
     [tokens, topk]) for dy [tokens, hidden]."""
     lib = _lib.load()
-    (_, h), n = _sizes("dy", dy), plan.tokens * plan.topk
-    lddy = _ld("dy", dy, plan.tokens, h, dy.dtype, dy)
+    (rows, h, lddy), n = _matrix("dy", dy), plan.tokens * plan.topk
+    if rows != plan.tokens:
+        raise _mismatch("dy", dy, plan.tokens, h)
     ldys = _ld("ys", ys, n, h, dy.dtype, dy)
     ldw = _ld("weights", weights, plan.tokens, plan.topk, torch.float32, dy)
     dt = _dtype(dy, "dy")
@@ -275,20 +285,25 @@ def _check_weight(w: QTensor | ExpertWeights, n_experts: int, like: torch.Tensor
                      f"{size * many} bytes on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _product(x, w, rows, n_experts, out_dtype, out):
+def _product(x, w, rows, k, n_experts, out_dtype, out):
     """What linear and expert_linear share: checks, output, workspace (a tensor to hold, see _address)."""
-    ldx = _ld("x", x, rows, w.k, x.dtype, x)
-    dt = _dtype(x, "x")
+    if k != w.k:
+        raise _mismatch("x", x, rows, w.k)
+    dt = odt = _dtype(x, "x")
     if out is None:
-        out = x.new_empty(rows, w.rows) if out_dtype is None else x.new_empty((rows, w.rows), dtype=out_dtype)
         ldo = w.rows
+        if out_dtype is None:
+            out = x.new_empty(rows, ldo)
+        else:
+            out = x.new_empty((rows, ldo), dtype=out_dtype)
+            odt = _dtype(out, "out")
     else:
         ldo = _ld("out", out, rows, w.rows, out_dtype or out.dtype, x)
-    odt = _dtype(out, "out")
+        odt = _dtype(out, "out")
     nb = _linear_workspace(rows, dt, w.fmt, w.block, w.layout, w.g_stripe, w.rows, w.k, n_experts, x.get_device())
     _check_weight(w, n_experts, x)
     ws = x.new_empty(nb, dtype=torch.uint8) if nb else None
-    return ldx, dt, out, ldo, odt, ws, nb
+    return dt, out, ldo, odt, ws, nb
 
 
 @_on_its_device
@@ -297,8 +312,8 @@ def linear(x: torch.Tensor, w: QTensor, out_dtype=None, out: torch.Tensor | None
     transposed, [rows, n] in out_dtype (x's by default). The transposed operand of a TILE2D weight
     gives the gradient dX = dY . W."""
     lib = _lib.load()
-    rows, _ = _sizes("x", x)
-    ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, 0, out_dtype, out)
+    rows, k, ldx = _matrix("x", x)
+    dt, out, ldo, odt, ws, nb = _product(x, w, rows, k, 0, out_dtype, out)
     op = w.operand()
     _lib.check(lib.fp4_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), out.data_ptr(), odt, ldo, _address(ws),
                               nb, _stream_of(x)))
@@ -315,13 +330,13 @@ def expert_linear(x: torch.Tensor, w: ExpertWeights, plan: ExpertPlan | torch.Te
     lib = _lib.load()
     offsets = plan.offsets if isinstance(plan, ExpertPlan) else plan
     experts = w.n_experts
-    rows, _ = _sizes("x", x)
+    rows, k, ldx = _matrix("x", x)
     if (offsets.dtype is not torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous()
             or offsets.device != x.device):
         raise ValueError(f"offsets must be a contiguous int32 tensor of {experts + 1} elements on {x.device}")
     if isinstance(plan, ExpertPlan) and rows != plan.tokens * plan.topk:
         raise ValueError(f"x must have the plan's {plan.tokens * plan.topk} rows (tokens * topk), got {rows}")
-    ldx, dt, out, ldo, odt, ws, nb = _product(x, w, rows, experts, out_dtype, out)
+    dt, out, ldo, odt, ws, nb = _product(x, w, rows, k, experts, out_dtype, out)
     op = w.operand()
     _lib.check(lib.fp4_expert_linear(x.data_ptr(), dt, rows, ldx, ctypes.byref(op), experts, offsets.data_ptr(),
                                      out.data_ptr(), odt, ldo, _address(ws), nb, _stream_of(x)))

@@ -166,7 +166,7 @@ def test_calls_run_with_their_tensors_device_current(monkeypatch):
 
         def __exit__(self, *exc):
             now[0] = self.before
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(experts, "_current_device", lambda: now[0])
     monkeypatch.setattr(torch.cuda, "device", Device)
 
     @experts._on_its_device
