@@ -266,6 +266,8 @@ fp4_status check_wlinear(const fp4_operand* w, int64_t rows, int32_t x_dtype, in
   a.K = w->k;
   a.n_experts = n_experts ? n_experts : 1;
   a.offsets_given = n_experts != 0;
+  if (!fp4k::wlinear_fits(a))
+    return fail(FP4_EUNSUPPORTED, "%s: more tiles of rows, N and experts than one launch holds", what);
   return FP4_OK;
 }
 

@@ -74,6 +74,7 @@ struct WLinearArgs {
   void* ws;
   hipStream_t stream;
 };
+bool wlinear_fits(const WLinearArgs& a);   // its tiles are no more than one launch holds (from the sizes, as below)
 size_t wlinear_ws(const WLinearArgs& a);   // bytes of WLinearArgs::ws (x, y and offsets are not looked at)
 hipError_t run_wlinear(const WLinearArgs& a);
 

@@ -758,8 +758,12 @@ __global__ __launch_bounds__(256) void k_zero_rows(char* y, int64_t rows, int64_
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Rows per expert (on average) from which the tile form is used.
-bool use_tile(const WLinearArgs& a) { return a.rows / a.n_experts > 16; }
+// A grid holds less than 2^32 threads; what is more is cut off without an error.
+constexpr int64_t MAX_THREADS = (int64_t(1) << 32) - 1;
+
+// The tile form is used from these many rows per expert (on average) on, and for weights of more rows
+// than a grid of the rows form holds (8 threads to each row of such a weight).
+bool use_tile(const WLinearArgs& a) { return a.rows / a.n_experts > 16 || a.N * 8 > MAX_THREADS - 512; }
 
 struct TilePlan {
   int tm;          // 32-row products per tile
@@ -791,6 +795,9 @@ TilePlan plan_tiles(const WLinearArgs& a) {
   }
   return best;
 }
+
+// workgroups of a plan, whole rounds of the eight dies
+int64_t tile_grid(const TilePlan& t) { return div_up(t.mt * t.nt * t.slices, 8) * 8; }
 
 // the bf16 parts of float32 activations, at the start of the workspace
 size_t planes_bytes(const WLinearArgs& a) { return a.x_f32 ? (size_t)div_up(3 * a.rows * a.K * 2, 256) * 256 : 0; }
@@ -840,7 +847,7 @@ void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
     t.part = reinterpret_cast<float*>((char*)a.ws + planes_bytes(a));
     t.f.y_vec = a.N % 4 == 0;
   }
-  const uint32_t grid = (uint32_t)(div_up(plan.mt * plan.nt * plan.slices, 8) * 8);
+  const uint32_t grid = (uint32_t)tile_grid(plan);
   auto go = [&](auto tm_) {
     constexpr int TM = decltype(tm_)::value;
     if (bytes) {
@@ -874,6 +881,12 @@ void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
 }
 
 }  // namespace
+
+bool wlinear_fits(const WLinearArgs& a) {
+  if (a.rows == 0 || a.N == 0 || a.K == 0 || !use_tile(a)) return true;
+  const TilePlan t = plan_tiles(a);
+  return tile_grid(t) * (t.tm == 8 ? 512 : 256) <= MAX_THREADS;
+}
 
 // the bf16 parts of float32 activations and the sums of a split K
 size_t wlinear_ws(const WLinearArgs& a) {

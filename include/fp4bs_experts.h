@@ -100,6 +100,9 @@ fp4_status fp4_expert_combine_grad(const void* dy, int32_t dtype, int64_t tokens
  *            one expert's (N * K / 2; N * K / block or N * K / 256; 1 or ceil(N / g_stripe) floats)
  *   offsets  device int32 [n_experts + 1], ascending from 0, at most rows (fp4_expert_sort)
  * n_experts in [1, 1024]. Weights of experts without rows are not read.
+ *
+ * Either call returns FP4_EUNSUPPORTED where its output tiles (of at least 32 x 256, and one more row of
+ * tiles to an expert) are 2^23 or more: rows * N or n_experts * N above 2^31 may be so many.
  */
 fp4_status fp4_linear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx, const fp4_operand* w, void* y,
                       int32_t y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);

@@ -279,3 +279,25 @@ def test_every_form_of_a_weight_is_taken(count, record):
     if count:
         with pytest.raises(ValueError, match="payload"):             # an expert's codes must follow each other
             fp4.expert_linear(x, replaced(weights[0], q=torch.zeros((3, 40, 64), dtype=torch.uint8)), plan_of())
+
+
+# ------------------------------------------------------------------ sizes
+
+def test_products_refuse_more_tiles_than_a_launch_holds():
+    """A grid of 2^32 threads or more is cut off without an error, so the library refuses it from the sizes alone."""
+    lib, nb = _lib.load(), ctypes.c_size_t()
+
+    def workspace(rows, n, k, count, dtype=0):
+        op = _lib.Operand(None, None, None, fp4.E8M0, 32, fp4.FP4_SCALES_1D, 0, n, k)
+        return lib.fp4_linear_workspace(rows, dtype, ctypes.byref(op), count, ctypes.byref(nb))
+    assert workspace(1, 2 ** 31 - 1, 64, 0) == _lib.FP4_OK
+    assert workspace(20, 2 ** 31 - 1, 64, 0) == _lib.FP4_OK
+    assert workspace(2 ** 20, 2 ** 17, 64, 0) == _lib.FP4_OK           # 2^21 tiles of 256 x 256
+    assert workspace(1024, 2 ** 22, 64, 1024) == _lib.FP4_OK           # few rows: no tiles
+    assert workspace(1, 2 ** 30, 64, 0) == _lib.FP4_OK
+    assert workspace(17 * 1024, 2 ** 23, 64, 1024) == _lib.FP4_EUNSUPPORTED
+    assert "one launch" in lib.fp4_last_error().decode()
+    op = _lib.Operand(4096, 4096, None, fp4.E8M0, 32, fp4.FP4_SCALES_1D, 0, 2 ** 23, 64)
+    p = ctypes.c_void_p(4096)
+    assert lib.fp4_expert_linear(p, 0, 17 * 1024, 64, ctypes.byref(op), 1024, p, p, 0, 2 ** 23, p, 1 << 40,
+                                 None) == _lib.FP4_EUNSUPPORTED

@@ -61,3 +61,24 @@ def test_smallest_float32_activations(m):
         y = fp4.linear(torch.from_numpy(x).cuda(), one_product_weight([2] * 24, [127] * 24)).cpu().numpy()
         err = np.abs(y.astype(np.float64) - x[:, 17].astype(np.float64)[:, None])
         assert (err == 0).all() if e >= -110 else (err < 2.0 ** -133).all(), e
+
+
+@pytest.mark.parametrize("dtype,n", [(torch.float32, 2 ** 29 + 16), (torch.bfloat16, 2 ** 30 + 16)])
+@pytest.mark.parametrize("m", [1, 17])
+def test_more_weight_rows_than_one_launch_of_the_rows_form_holds(m, dtype, n):
+    """A grid holds less than 2^32 threads: from 2^29 weight rows on (2^30 for bf16 activations) one row of
+    activations needs another form than few rows usually take."""
+    import fp4_block_scaled_tensor_amd as fp4
+    k = 64
+    q = torch.zeros((n, k // 2), dtype=torch.uint8, device="cuda")
+    rows = [0, 255, 256, 2 ** 28 + 1, n - 17, n - 1]
+    for i, row in enumerate(rows):
+        q[row, 3] = 2 + i                                    # E2M1 code 2 + i at k = 6
+    w = fp4.QTensor(q, torch.full((n, 2), 127, dtype=torch.uint8, device="cuda"), torch.ones(1, device="cuda"), fp4.E8M0,
+                    32, fp4.FP4_SCALES_1D, n, k)
+    x = torch.zeros((m, k), dtype=dtype, device="cuda")
+    x[:, 6] = torch.arange(1, m + 1, device="cuda")
+    y = fp4.linear(x, w, out_dtype=torch.bfloat16)
+    want = torch.arange(1, m + 1)[:, None] * torch.from_numpy(OF.E2M1_VALUES[[2 + i for i in range(6)]])
+    assert torch.equal(y[:, rows].cpu().double(), want.to(torch.bfloat16).double())
+    assert torch.count_nonzero(y[-1]) == len(rows) and torch.count_nonzero(y[0]) == len(rows)
