@@ -476,7 +476,9 @@ struct TileForm {
   // eight waves of 256 x 32 outputs for the tallest tile, else four of 32 TM x 64
   static constexpr int NW = TM == 8 ? 8 : 4, TN = TILE_BN / 32 / NW;
   static constexpr int BM = TM * 32, STAGE = BM * ROWB, PIECES = BM / 8 / NW;
-  static constexpr int NXB = TM == 8 ? 3 : 2;              // three would take the second workgroup's LDS below 8
+  // Three below 8 would take the LDS of a second workgroup, and gave little where there is only one: 77
+  // rows 28672 x 4096 MXFP4 46.1 -> 44.0 us, 4096 x 14336 the same, 20 rows 31.1 -> 31.4.
+  static constexpr int NXB = TM == 8 ? 3 : 2;
   using Weight = WeightTurns<B, BYTES_, TN * 2>;
   static constexpr int WBYTES = 2 * Weight::SIZE;          // a wave's two turns
   static constexpr int OW = TN * 32, OLD = OW + 4;         // a wave's output columns, padded by 16 bytes
@@ -761,8 +763,13 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // A grid holds less than 2^32 threads; what is more is cut off without an error.
 constexpr int64_t MAX_THREADS = (int64_t(1) << 32) - 1;
 
-// The tile form is used from these many rows per expert (on average) on, and for weights of more rows
-// than a grid of the rows form holds (8 threads to each row of such a weight).
+// The tile form is used from more than 16 rows per expert (on average) on, and for weights of more rows
+// than a grid of the rows form holds (8 threads to each row of such a weight). Measured, us in the rows
+// form / the tile form. Eight experts 14336 x 4096, 16 rows each: MXFP4 86.7 / 89.1, UE5M3 105 / 97; 24
+// rows 104 / 109, 128 / 119. One weight, 20 rows: 28672 x 4096 MXFP4 30.2 / 31.1, UE5M3 40.1 / 34.8; 64
+// rows 53.9 / 43.2, 71.0 / 47.5. Where there are few tiles the rows form would be ahead for longer: 4096 x
+// 4096, 20 rows 8.5 / 16.1, 64 rows 13.6 / 24.2; 4096 x 14336, 20 rows 20.8 / 27.2, 64 rows 39.6 / 33.8.
+// float32 activations, 17 rows (20 in the tile form): 28672 x 4096 64 / 49, 4096 x 4096 16 / 23.
 bool use_tile(const WLinearArgs& a) { return a.rows / a.n_experts > 16 || a.N * 8 > MAX_THREADS - 512; }
 
 struct TilePlan {
@@ -809,7 +816,9 @@ void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
   const bool bytes = f.s_k != 1 || (B == 32 && a.K % TURN_K != 0);
   if (!use_tile(a)) {
     const uint32_t groups = a.offsets ? a.n_experts + 1 : 1;
-    // as many products to an activation fragment as leave no compute unit without a workgroup
+    // As many products to an activation fragment as leave no compute unit without a workgroup. Measured,
+    // us with 1 / 2 / 4, MXFP4, 4 rows: 4096 x 4096 5.4 / 6.7 / 8.4, 28672 x 4096 21.8 / 19.2 / 19.1 (16
+    // rows: 34.6 / 24.2 / 21.7).
     const int64_t cus = device_cu_count(), each = a.n_experts;
     const int tn = PLANES == 1 && div_up(a.N, 64) * each >= cus ? 4 : div_up(a.N, 32) * each >= cus ? 2 : 1;
     auto go = [&](auto tn_, auto xr_, auto bytes_) {
@@ -818,11 +827,14 @@ void launch(const WLinearArgs& a, const WParams& p, const FormArgs& f) {
       k_wlinear_rows<F><<<grid, F::NW * 64, 0, a.stream>>>(p, f);
     };
     auto with_bytes = [&](auto tn_, auto xr_) { bytes ? go(tn_, xr_, std::true_type{}) : go(tn_, xr_, std::false_type{}); };
-    // Activation rows at a time. An expert with more rows than that reads its weight again (from the
-    // caches); rows that are not there cost copies and LDS: 16 slots over 8 experts took 73 us with
-    // 16 rows at a time.
+    // Activation rows at a time. A group with more rows reads its weight again (from the caches); rows that
+    // are not there cost copies and LDS. Measured, us with 4 / 8 / 16 at a time, MXFP4: one weight 28672 x
+    // 4096, 1 row 18.5 / 18.9 / 19.4, 5 rows 28.6 / 19.4 / 20.0, 9 rows 38.0 / 29.5 / 20.6. Experts with rows
+    // by chance have more than the average in some: eight of 14336 x 4096, on average 1 row 45.6 / 47.1 /
+    // 48.6, 2 rows 56.1 / 51.9 / 53.8, 4 rows 65.8 / 57.1 / 59.4, 6 rows 92.2 / 64.8 / 62.0; 64 of 1024 x
+    // 2048, 1 row 13.8 / 14.1 / 14.5, 2 rows 19.5 / 17.7 / 18.2, 5 rows 27.9 / 22.1 / 19.5.
     const int64_t avg = div_up(a.rows, a.n_experts);
-    const int xr = a.offsets ? (avg <= 2 ? 4 : avg <= 5 ? 8 : 16) : (avg <= 4 ? 4 : avg <= 8 ? 8 : 16);
+    const int xr = a.offsets ? (avg <= 1 ? 4 : avg <= 4 ? 8 : 16) : (avg <= 4 ? 4 : avg <= 8 ? 8 : 16);
     auto with_rows = [&](auto tn_) {
       if constexpr (PLANES == 1) {
         if (xr == 4) return with_bytes(tn_, integral_constant<int, 4>{});
