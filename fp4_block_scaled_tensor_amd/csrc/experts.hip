@@ -87,12 +87,6 @@ __device__ __forceinline__ void wave_count(const uint32_t* key, int lo, int hi, 
     if (lo + i * 64 + (int)(threadIdx.x & 63) < hi) atomicAdd(&row[key[i]], 1);
 }
 
-// Keeps the wave's LDS accesses in program order (the LDS itself serves a wave's accesses in order).
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Places them: row[key] is the wave's next position of each key.
 template <int NK>
 __device__ __forceinline__ void wave_place(const uint32_t* keys, int E, int bits, int lo, int hi, int* row,
@@ -465,8 +459,6 @@ __global__ __launch_bounds__(MT) void k_combine_grad(const char* __restrict__ dy
 bool vec_ok(const void* p, int64_t ld, int64_t esz) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * esz) % 16 == 0;
 }
-
-int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // f(F32, ALIGNED) with both as compile-time constants
 template <class F>

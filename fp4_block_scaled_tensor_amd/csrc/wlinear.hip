@@ -63,12 +63,6 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
 // this wave's copies have landed and its LDS reads are done
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
-// Orders a wave's LDS writes before its other lanes' reads (the LDS serves a wave in order).
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 template <bool E8, int SEL>
 __device__ __forceinline__ uint32_t decode_pair(uint32_t w, float sv) {
   if constexpr (E8) {
@@ -254,8 +248,11 @@ struct WeightTurns {
 // turns are in flight while one is multiplied. Activation rows past the group repeat its last one;
 // their products, and those of the 16 - XR rows of a product that are not there, are not stored.
 // Activation row r (256 bytes) keeps its 16-byte piece j at j ^ r % 16, against bank conflicts.
-// Measured: 114688 x 4096 MXFP4, one row, 54 us (4.6 TB/s); 28672 x 4096 18.6 us, 5 to 6 us of it launch
-// and ramp; 4096 x 4096 4.5 us. Three-mantissa-bit scales add the decode, 28672 x 4096 UE5M3 23 us.
+// Measured, one row, MXFP4: 114688 x 4096 54 us (4.6 TB/s); 28672 x 4096 18.5 us, 5 to 6 us of it launch
+// and ramp; 4096 x 4096 5.4 us (4.5 with three weights in turn, which the L2 holds). Three-mantissa-bit
+// scales add the decode: 28672 x 4096 UE5M3 21.0 us with 2D scales, 24.4 us with a row of scales to each
+// weight row, whose few bytes a turn are a line each. float32 rows, always 16 at a time and in three
+// planes: 28672 x 4096 MXFP4 33 us for one, 41 us for 16.
 template <bool E8_, int B_, int PLANES_, int TN_, int XR_, bool BYTES_>
 struct RowsForm {
   static constexpr bool E8 = E8_, BYTES = BYTES_;
@@ -392,8 +389,8 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
 // A workgroup owns a BM x 256 tile of one expert's outputs: four waves, each all BM = 32 TM rows of
 // x and 64 of the weight's rows (TM x 2 products of 32x32x16), or for BM = 256 eight waves with 32 of
 // the weight's rows each, two to a SIMD. K advances in steps of 64. Bound by the matrix cores, which
-// are busy 66% of the cycles (8192 rows over eight experts, 4096 -> 14336, MXFP4: 0.92 ms; a plain
-// 8192 x 4096 -> 14336 product 758 us, 1.27 PFLOP/s, the library's bf16 product 650 us).
+// are busy 65% of the cycles (8192 rows over eight experts, 4096 -> 14336, MXFP4: 0.88 to 0.92 ms; a
+// plain 8192 x 4096 -> 14336 product 754 us, 1.28 PFLOP/s, the library's bf16 product 645 us).
 //
 // A wave needs its weight rows for itself alone, so it copies their codes and scales a turn of 128 k
 // at a time and decodes them in registers: lane l holds row l % 32 and the 32 codes of K half l / 32
@@ -670,7 +667,7 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
         for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r4 * 4 + r];
         *reinterpret_cast<v4f*>(out + fr * OLD + i * 32 + r4 * 8 + fk * 4) = v;
       }
-    wave_lds_order();
+    wave_order();
 #pragma unroll 4
     for (int o = lane; o < 32 * OW / 4; o += 64) {
       const int r = o / (OW / 4), c = (o % (OW / 4)) * 4;
@@ -689,7 +686,7 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
           if (n + q < p.N) y_f32 ? store1<true>(y, at + q, v[q] * gn) : store1<false>(y, at + q, v[q] * gn);
       }
     }
-    wave_lds_order();
+    wave_order();
   }
 }
 
@@ -757,8 +754,6 @@ __global__ __launch_bounds__(256) void k_zero_rows(char* y, int64_t rows, int64_
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * n; i += (int64_t)gridDim.x * 256)
     store1<F32>(y, i / n * ldy + i % n, 0.0f);
 }
-
-int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // A grid holds less than 2^32 threads; what is more is cut off without an error.
 constexpr int64_t MAX_THREADS = (int64_t(1) << 32) - 1;
