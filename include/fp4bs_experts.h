@@ -80,7 +80,8 @@ fp4_status fp4_expert_combine_grad(const void* dy, int32_t dtype, int64_t tokens
  *   x        device, [rows x K] of x_dtype, row stride ldx elements (16-byte aligned rows)
  *   w        the weight: any format, block, scale layout and g (NULL, one float or stripes) that
  *            the GEMMs take; N = w->rows, K = w->k. The forward view of a weight gives X . W^T,
- *            the transposed view (FP4_SCALES_2D_T) of the same weight dX = dY . W. Scale
+ *            the transposed view (FP4_SCALES_2D_T) of the same weight dX = dY . W; with 1D scales
+ *            dX takes the weight's COL view (FP4_VIEW_COL), quantized for itself. Scale
  *            codes 4-byte aligned; K and ldx at most 2^22, rows and N below 2^31.
  *   y        device, [rows x N] of y_dtype, row stride ldy elements (>= N; element aligned)
  *   ws       device workspace of at least the bytes fp4_linear_workspace gives (16-byte aligned;

@@ -145,3 +145,21 @@ def test_one_band_of_a_two_dimensional_grid(dtype, layout, n, m):
     x64 = r.integers(-8, 9, (m, k)).astype(np.float64)
     y = fp4.linear(torch.from_numpy(x64).to(DT[dtype]).cuda(), w, out_dtype=torch.float32)
     assert np.array_equal(y.cpu().double().numpy(), x64 @ w64.T)
+
+
+@pytest.mark.parametrize("m", [4, 80])
+@pytest.mark.parametrize("fmt,block", [("e8m0", 32), ("ue5m3", 16)])
+def test_gradient_through_the_col_view(fmt, block, m):
+    """A weight with 1D scales: dX = dY . W from the weight's COL view."""
+    import fp4_block_scaled_tensor_amd as fp4
+    r, n, k = gen(m), 192, 320
+    w = torch.from_numpy(r.integers(-6, 7, (n, k)).astype(np.float32)).cuda()
+    f = {"e8m0": fp4.E8M0, "ue5m3": fp4.UE5M3}[fmt]
+    wt = fp4.quantize(w, f, block, fp4.COL, amax=None if fmt == "e8m0" else fp4.tensor_amax(w))
+    w64 = fp4.dequantize(wt).double().cpu().numpy()              # [k, n]
+    # the quantized weight is the weight to within half a step of E2M1 (2 between 4 and 6 sixths of the maximum) and
+    # the rounding of a 3-mantissa-bit scale (a sixteenth)
+    assert np.abs(w64 - w.cpu().double().numpy().T).max() <= 6 * (1 / 6 + 1 / 16)
+    dy = r.integers(-4, 5, (m, n)).astype(np.float64)
+    dx = fp4.linear(torch.from_numpy(dy).to(torch.bfloat16).cuda(), wt, out_dtype=torch.float32)
+    close(dx, dy, w64, 1.0, torch.float32, "dx")
