@@ -19,6 +19,7 @@
 #pragma once
 #include "fp4_device.hpp"
 #include "launch.hpp"
+#include "lds_copy.hpp"
 #include "quant_common.hpp"
 
 namespace fp4k {
@@ -52,26 +53,6 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 // chunk position of logical 16-byte chunk `chunk` in LDS row `row`
 __device__ __forceinline__ int swz_pos(int row, int chunk) { return chunk ^ ((row >> FP4_SWZ_SHIFT) & 7); }
 __device__ __forceinline__ int swz(int row, int chunk) { return row * ROWB + (swz_pos(row, chunk) << 4); }
-
-// LDS byte address of a pointer into a __shared__ array (a generic pointer to LDS keeps the
-// LDS offset in its low 32 bits).
-__device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p); }
-
-// One global_load_lds_dwordx4 for the wave: lane i copies the 16 bytes at sbase + voff(i)
-// to LDS bytes [dst + 16 i, dst + 16 i + 16) (dst is wave-uniform and goes in M0, with the
-// one-instruction gap the M0 write needs before the load). Written as inline assembly so
-// that the compiler's wait-count insertion does not treat the copy as an LDS write that may
-// alias later LDS reads of the other buffer: the kernels wait for these copies themselves
-// (vmcnt(0) and a barrier before the buffer is read).
-__device__ __forceinline__ void lds_dma16(const uint8_t* sbase, uint32_t voff, uint32_t dst) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 1\n\t"
-      "global_load_lds_dwordx4 %0, %1"
-      :
-      : "v"(voff), "s"(sbase), "s"(dst)
-      : "memory", "m0");
-}
 
 // Direct global->LDS loads of one stage of a ROWS-row payload tile by NW waves. Each wave
 // fills P = ROWS / (8 NW) contiguous 1024-byte LDS pieces; lane i of piece p writes LDS

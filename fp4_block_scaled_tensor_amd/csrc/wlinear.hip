@@ -7,6 +7,7 @@
 // larger E2M1 values, and those weights are infinite.) A float32 activation is split into three bf16
 // parts (8 + 8 + 8 significant bits by truncation), each multiplied into the same sums.
 #include "experts.hpp"
+#include "lds_copy.hpp"
 
 namespace fp4k {
 
@@ -18,37 +19,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
-// One 16-byte copy per lane from base + off (base wave-uniform) to LDS at dst + 16 * lane, without
-// registers in between. Inline assembly, so that the compiler does not wait for it before LDS reads
-// of the other buffer; wait_copies() and a barrier come before the copied bytes are read.
-__device__ __forceinline__ void dma16(const char* base, uint32_t off, char* dst) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 1\n\t"
-      "global_load_lds_dwordx4 %0, %1"
-      :
-      : "v"(off), "s"(base), "s"((uint32_t)reinterpret_cast<uintptr_t>(dst))
-      : "memory", "m0");
-}
-// The same for one dword, or for one byte (zero-extended to a dword), per lane: LDS at dst + 4 * lane.
-__device__ __forceinline__ void dma4(const char* base, uint32_t off, char* dst) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 1\n\t"
-      "global_load_lds_dword %0, %1"
-      :
-      : "v"(off), "s"(base), "s"((uint32_t)reinterpret_cast<uintptr_t>(dst))
-      : "memory", "m0");
-}
-__device__ __forceinline__ void dma1(const char* base, uint32_t off, char* dst) {
-  asm volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 1\n\t"
-      "global_load_lds_ubyte %0, %1"
-      :
-      : "v"(off), "s"(base), "s"((uint32_t)reinterpret_cast<uintptr_t>(dst))
-      : "memory", "m0");
-}
 // all but the newest N of the wave's copies have landed
 template <int N>
 __device__ __forceinline__ void wait_all_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
@@ -210,15 +180,15 @@ struct WeightTurns {
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       const int piece = (lane & 3) ^ (((j * 16 + (lane >> 2)) >> 2) & 3);
-      dma16(src, cut && (piece & 2) ? qoff[j] - 32 : qoff[j], to + j * 1024);
+      lds_dma16(src, cut && (piece & 2) ? qoff[j] - 32 : qoff[j], lds_offset(to + j * 1024));
     }
     src = sbase + turn * s_turn;
 #pragma unroll
     for (int j = 0; j < NSC; ++j) {
       const uint32_t step = BYTES ? (uint32_t)(s_turn / 2) : 4;
       const uint32_t off = cut && PER > 1 && (lane % PER) >= PER / 2 ? soff[j] - step : soff[j];
-      if constexpr (BYTES) dma1(src, off, to + SCALES + j * 256);
-      else dma4(src, off, to + SCALES + j * 256);
+      if constexpr (BYTES) lds_dma1(src, off, lds_offset(to + SCALES + j * 256));
+      else lds_dma4(src, off, lds_offset(to + SCALES + j * 256));
     }
   }
   // the 32 codes of piece j (32 k) of a row, and their scale codes (two at block 16)
@@ -309,7 +279,7 @@ __global__ __launch_bounds__(F::NW * 64) void k_wlinear_rows(WParams p, FormArgs
 #pragma unroll
         for (int j = 0; j < XR / 4; ++j) {
           const int piece = (lane & 15) ^ (j * 4 + (lane >> 4));
-          dma16(src, cut && (piece & 8) ? xoff[j] - 128 : xoff[j], to + F::XROWS + (o * (XR / 4) + j) * 1024);
+          lds_dma16(src, cut && (piece & 8) ? xoff[j] - 128 : xoff[j], lds_offset(to + F::XROWS + (o * (XR / 4) + j) * 1024));
         }
       }
     };
@@ -536,7 +506,7 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_wlinear_tile(WParams p, TileA
   int xplane = 0;
   auto copy_x = [&](char* buf) {
 #pragma unroll
-    for (int j = 0; j < PIECES; ++j) dma16(xsrc, xoff[j], buf + (wave * PIECES + j) * 1024);
+    for (int j = 0; j < PIECES; ++j) lds_dma16(xsrc, xoff[j], lds_offset(buf + (wave * PIECES + j) * 1024));
     if (PLANES == 1) {
       xsrc += ROWB;
     } else {
