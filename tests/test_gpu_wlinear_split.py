@@ -113,3 +113,28 @@ def test_split_k_over_experts(counts, n, dropped, fmt, block, layout, dtype):
         if a < b:
             want = (x[a:b].double() @ torch.from_numpy(w64.T.copy()).cuda()) * 2.0 ** e
             assert torch.equal(y[a:b].double(), want), e
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [64, 19, 1])
+@pytest.mark.parametrize("experts", [1, 2, 62, 63, 64, 65, 130])
+def test_g_of_many_experts(experts, n, out):
+    """Each row gets its own expert's g, rows of empty and of one-row experts next to each other; exact on integers."""
+    import fp4_block_scaled_tensor_amd as fp4
+    from test_gpu_experts import gen
+    r, k = gen(experts), 512
+    counts = r.choice([0, 1, 2, 40], experts, p=[0.2, 0.2, 0.2, 0.4])
+    counts[-1] = 40
+    ends = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = max(int(ends[-1]) + 5, 17 * experts)
+    g = 2.0 ** np.arange(-(experts // 2), experts - experts // 2).clip(-30, 30)
+    w = ones_weight(n, k, 1.0)
+    stack = fp4.ExpertWeights(w.q.expand(experts, -1, -1).contiguous(), w.s.expand(experts, -1, -1).contiguous(),
+                              torch.tensor(g, dtype=torch.float32, device="cuda").view(-1, 1), w.fmt, 16, w.layout, n, k)
+    assert workspace_slices(rows, stack, experts) > 1
+    x64 = r.integers(-4, 5, (rows, k)).astype(np.float64)
+    y = fp4.expert_linear(torch.from_numpy(x64).to(torch.bfloat16).cuda(), stack, torch.from_numpy(ends).cuda(),
+                          out_dtype=DT[out])
+    scale = np.concatenate([np.repeat(g, counts), np.zeros(rows - int(ends[-1]))])
+    want = np.repeat((x64.sum(1) * scale)[:, None], n, 1).astype(np.float32)
+    assert torch.equal(y.cpu(), torch.from_numpy(want).to(DT[out]))
