@@ -69,3 +69,26 @@ def test_sort_of_almost_2_to_the_31_slots():
         slot = p + 1 + (p + 1 >= mid)
         assert torch.equal(order[lo:hi].long(), slot), lo
         assert torch.equal(pos[slot].long(), p), lo
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sums_keep_subnormals(dtype):
+    """Subnormal rows come through the sums and the gradients: with one slot to a token and weights of 1 every output
+    is its input; two equal slots double it (exactly, also where the result is subnormal)."""
+    import fp4_block_scaled_tensor_amd as fp4
+    kind, word, count = (torch.bfloat16, torch.int16, 127) if dtype == "bf16" else (torch.float32, torch.int32, 2 ** 23 - 1)
+    bits = torch.arange(1, count + 1, max(1, count // 4000), dtype=torch.int64)
+    bits = torch.cat([bits, bits + (2 ** 15 if dtype == "bf16" else 2 ** 31)])                    # both signs
+    bits = torch.where(bits >= 2 ** (8 * word.itemsize - 1), bits - 2 ** (8 * word.itemsize), bits).to(word)
+    rows = bits.view(kind).repeat(2, 1).cuda()
+    one = fp4.expert_sort(torch.tensor([[1], [0]], dtype=torch.int32, device="cuda"), 2)
+    w = torch.ones((2, 1), device="cuda")
+    flip = rows.flip(0)
+    same = lambda a, b: torch.equal(a.contiguous().view(word), b.contiguous().view(word))   # noqa: E731
+    assert same(fp4.expert_gather_grad(rows, one), flip) and same(fp4.expert_combine(rows, w, one), flip)
+    dys, _ = fp4.expert_combine_grad(rows, rows, w, one)
+    assert same(dys, flip)
+    two = fp4.expert_sort(torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"), 2)
+    twice = (rows[:1].double() * 2).to(kind)
+    assert same(fp4.expert_gather_grad(rows, two), twice)
+    assert same(fp4.expert_combine(rows, torch.ones((1, 2), device="cuda"), two), twice)

@@ -82,3 +82,20 @@ def test_more_weight_rows_than_one_launch_of_the_rows_form_holds(m, dtype, n):
     want = torch.arange(1, m + 1)[:, None] * torch.from_numpy(OF.E2M1_VALUES[[2 + i for i in range(6)]])
     assert torch.equal(y[:, rows].cpu().double(), want.to(torch.bfloat16).double())
     assert torch.count_nonzero(y[-1]) == len(rows) and torch.count_nonzero(y[0]) == len(rows)
+
+
+@pytest.mark.parametrize("m", [3, 40, 300])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_subnormal_outputs(m, dtype):
+    """Products below 2^-126: exact in float32, rounded to nearest in bfloat16."""
+    import fp4_block_scaled_tensor_amd as fp4
+    codes, scales = (v.reshape(-1) for v in np.meshgrid(np.arange(16), np.arange(0, 9)))
+    w64 = OF.E2M1_VALUES[codes] * 2.0 ** (scales.astype(np.float64) - 127)
+    x = rows_of([1.0, -1.5, 0.25, 1.9921875, 2.0 ** -8], m)              # 8 significant bits: exact in bf16
+    want = x[:, 17].astype(np.float64)[:, None] * w64[None]
+    w = one_product_weight(codes, scales)
+    xd = torch.from_numpy(x).to(dtype).cuda()
+    y = fp4.linear(xd, w, out_dtype=torch.float32).cpu().double().numpy()
+    assert np.array_equal(y, want)                                          # multiples of 2^-149 all
+    y = fp4.linear(xd, w, out_dtype=torch.bfloat16).cpu().double()
+    assert torch.equal(y, torch.from_numpy(want).to(torch.float32).to(torch.bfloat16).double())
