@@ -204,7 +204,7 @@ def _scales(amax, scale):
     one = torch.ones((), device=amax.device)
     a = amax.clamp_min(2.0 ** -100)
     s = torch.where(amax > 0, a / 448.0, one)
-    return torch.where(amax > 0, 448.0 / a, one), s, s
+    return torch.where(amax > 0, torch.full_like(a, 448.0) / a, one), s, s
 
 
 def _pad(x, rows, cols):
