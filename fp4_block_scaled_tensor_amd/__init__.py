@@ -25,7 +25,9 @@ __all__ = ["UE5M3", "E4M3", "E8M0", "ROW", "COL", "TILE2D", "QTensor", "AmaxCach
            "gemm_fprop", "gemm_dgrad", "gemm_wgrad", "gemm_fprop_q", "gemm_dgrad_q", "decode_f16", "gemm_f16", "scale_range", "check_range", "new_stats", "debug_encode",
            "FP4Error", "library",
            "ExpertPlan", "ExpertWeights", "stack_experts", "expert_sort", "expert_gather", "expert_gather_grad",
-           "expert_combine", "expert_combine_grad", "linear", "expert_linear"]
+           "expert_combine", "expert_combine_grad", "linear", "expert_linear",
+           "F8_SCALE_E8M0", "F8_SCALE_F32", "F8Tensor", "F8Experts", "fp8_stack", "fp8_quantize", "fp8_quantize_rowcol",
+           "fp8_dequantize", "fp8_gemm", "fp8_expert_gemm", "fp8_gated", "gated_grad", "fp8_gated_grad"]
 
 
 def library() -> ctypes.CDLL:
@@ -451,3 +453,5 @@ def debug_encode(x: torch.Tensor, which: int, u16: torch.Tensor | None = None) -
 
 from .experts import (ExpertPlan, ExpertWeights, expert_combine, expert_combine_grad, expert_gather,  # noqa: E402
                       expert_gather_grad, expert_linear, expert_sort, linear, stack_experts)
+from .fp8 import (F8_SCALE_E8M0, F8_SCALE_F32, F8Experts, F8Tensor, fp8_dequantize, fp8_expert_gemm, fp8_gated,  # noqa: E402
+                  fp8_gated_grad, fp8_gemm, fp8_quantize, fp8_quantize_rowcol, fp8_stack, gated_grad)

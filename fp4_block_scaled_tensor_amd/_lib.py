@@ -13,6 +13,10 @@ FP4_UE5M3, FP4_E4M3, FP4_E8M0 = 0, 1, 2
 FP4_VIEW_ROW, FP4_VIEW_COL, FP4_VIEW_TILE2D = 0, 1, 2
 FP4_IN_BF16, FP4_IN_FP32 = 0, 1
 FP4_SCALES_1D, FP4_SCALES_2D, FP4_SCALES_2D_T = 0, 1, 2
+FP8_SCALE_E8M0, FP8_SCALE_F32 = 0, 1
+FP8_VIEW_ROWCOL = 3
+FP8_ACT_SILU, FP8_ACT_GELU, FP8_ACT_GELU_TANH = 0, 1, 2
+FP8_OUT_E4M3 = 2
 ABI_VERSION = 3
 
 EXPORTED = [
@@ -33,6 +37,11 @@ class Operand(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("g", ctypes.c_void_p),
                 ("fmt", ctypes.c_int32), ("block", ctypes.c_int32), ("scale_layout", ctypes.c_int32),
                 ("g_stripe", ctypes.c_int32), ("rows", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
+class F8Operand(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("scale", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("k", ctypes.c_int64)]
 
 
 class AmaxCacheC(ctypes.Structure):
@@ -92,6 +101,24 @@ EXPERTS_SIGNATURES = {
     "fp4_linear_workspace": ([_I64, _I32, ctypes.POINTER(Operand), _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
 }
 
+# include/fp4bs_fp8.h
+FP8_EXPORTED = [
+    "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_expert_gemm", "fp8_gated", "fp8_gemm_workspace", "gated_grad",
+    "fp8_gated_grad",
+]
+
+_F8 = ctypes.POINTER(F8Operand)
+FP8_SIGNATURES = {
+    "fp8_quantize": ([_P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _P, _P, _P, _P], ctypes.c_int),
+    "fp8_dequantize": ([_F8, _P, _I32, _I64, _P], ctypes.c_int),
+    "fp8_gemm": ([_F8, _F8, _P, _I32, _I64, _P, _SZ, _P], ctypes.c_int),
+    "fp8_expert_gemm": ([_F8, _F8, _I32, _P, _P, _I32, _I64, _P, _SZ, _P], ctypes.c_int),
+    "fp8_gated": ([_F8, _F8, _I32, _P, _I32, _P, _I32, _I64, _P, _P, _I32, _I64, _P, _SZ, _P], ctypes.c_int),
+    "fp8_gemm_workspace": ([_I64, _F8, _I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "gated_grad": ([_P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _P], ctypes.c_int),
+    "fp8_gated_grad": ([_P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _I32, _P, _P, _P, _P, _P], ctypes.c_int),
+}
+
 _lib = None
 
 
@@ -104,7 +131,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         raise ImportError(f"{path} is missing: build it with `python -m fp4_block_scaled_tensor_amd.build` "
                           "(the FP4 path has no CPU or PyTorch fallback)")
     lib = ctypes.CDLL(path)
-    for name, (args, res) in (SIGNATURES | EXPERTS_SIGNATURES).items():
+    for name, (args, res) in (SIGNATURES | EXPERTS_SIGNATURES | FP8_SIGNATURES).items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res

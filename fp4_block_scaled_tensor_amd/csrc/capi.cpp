@@ -8,7 +8,9 @@
 
 #include "../../include/fp4bs.h"
 #include "../../include/fp4bs_experts.h"
+#include "../../include/fp4bs_fp8.h"
 #include "experts.hpp"
+#include "fp8.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -300,6 +302,120 @@ fp4_status wlinear(const void* x, int32_t x_dtype, int64_t rows, int64_t ldx, co
   a.stream = (hipStream_t)stream;
   return hip_status(fp4k::run_wlinear(a), what);
 }
+
+// ---- the 8-bit operators (fp4bs_fp8.h) ----
+fp4_status check_f8_scale(int32_t scale, const char* what) {
+  if (scale != FP8_SCALE_E8M0 && scale != FP8_SCALE_F32) return fail(FP4_EINVAL, "%s: unknown scale type %d", what, scale);
+  return FP4_OK;
+}
+
+fp4_status check_io_dtype(int32_t dtype, const char* what, const char* name) {
+  if (dtype != FP4_IN_BF16 && dtype != FP4_IN_FP32) return fail(FP4_EINVAL, "%s: unknown %s dtype %d", what, name, dtype);
+  return FP4_OK;
+}
+
+// An E4M3 payload's and its scales' addresses.
+fp4_status check_f8_out(const void* q, const void* s, int32_t scale, const char* what, const char* name) {
+  if (!q || !s) return fail(FP4_EINVAL, "%s: NULL codes or scales of the %s", what, name);
+  if (!aligned(q, 16)) return fail(FP4_EALIGN, "%s: codes of the %s not 16-byte aligned", what, name);
+  if (scale == FP8_SCALE_F32 && !aligned(s, 4)) return fail(FP4_EALIGN, "%s: scales of the %s not 4-byte aligned", what, name);
+  return FP4_OK;
+}
+
+fp4_status check_f8_operand(const fp8_operand* o, bool pointers, const char* what, const char* name) {
+  if (!o) return fail(FP4_EINVAL, "%s: %s is NULL", what, name);
+  fp4_status st = check_f8_scale(o->scale, what);
+  if (st != FP4_OK) return st;
+  if (o->layout < FP4_SCALES_1D || o->layout > FP4_SCALES_2D_T)
+    return fail(FP4_EINVAL, "%s: %s: unknown scale layout %d", what, name, o->layout);
+  if (o->rows < 0 || o->k < 0) return fail(FP4_EINVAL, "%s: %s: negative size", what, name);
+  if (o->rows > MAX_SLOTS) return fail(FP4_EUNSUPPORTED, "%s: %s: rows must be below 2^31", what, name);
+  if (o->k > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: %s: k must be at most 2^22", what, name);
+  if (pointers && o->rows > 0 && o->k > 0) return check_f8_out(o->q, o->s, o->scale, what, name);
+  return FP4_OK;
+}
+
+fp4k::F8Operand f8_operand(const fp8_operand* o) {
+  return fp4k::F8Operand{o->q, o->s, o->scale == FP8_SCALE_E8M0, o->layout, o->rows, o->k};
+}
+
+// Fills a's operands and sizes; n_experts 0: one weight.
+fp4_status check_f8_product(const fp8_operand* x, const fp8_operand* w, int32_t n_experts, bool gated, bool pointers,
+                            const char* what, fp4k::F8GemmArgs& a) {
+  fp4_status st;
+  if ((st = check_f8_operand(x, pointers, what, "first operand")) != FP4_OK) return st;
+  if ((st = check_f8_operand(w, pointers, what, "second operand")) != FP4_OK) return st;
+  if (x->layout != FP4_SCALES_1D) return fail(FP4_EUNSUPPORTED, "%s: the first operand needs 1D scales", what);
+  if (x->k != w->k)
+    return fail(FP4_EINVAL, "%s: operands have different k (%lld vs %lld)", what, (long long)x->k, (long long)w->k);
+  if (x->scale != w->scale) return fail(FP4_EUNSUPPORTED, "%s: operands differ in scale type", what);
+  if (n_experts != 0 && (st = check_experts(n_experts, what)) != FP4_OK) return st;
+  if (gated && w->rows % 2) return fail(FP4_EINVAL, "%s: a gated weight has an even number of rows", what);
+  const int64_t blocks = (w->k + 127) / 128;
+  if (w->rows * blocks > (int64_t(1) << 30) - 1)   // offsets into its scales are 32 bits
+    return fail(FP4_EUNSUPPORTED, "%s: a weight of 2^37 bytes or more", what);
+  a.x = f8_operand(x);
+  a.w = f8_operand(w);
+  a.n_experts = n_experts ? n_experts : 1;
+  a.offsets_given = n_experts != 0;
+  a.gated = gated;
+  if (!fp4k::f8_gemm_fits(a)) return fail(FP4_EUNSUPPORTED, "%s: 2^23 output tiles or more", what);
+  return FP4_OK;
+}
+
+fp4_status f8_product(const fp8_operand* x, const fp8_operand* w, int32_t n_experts, const int32_t* offsets, void* y,
+                      int32_t y_kind, int64_t ldy, void* ws, size_t ws_bytes, void* stream, const char* what,
+                      fp4k::F8GemmArgs& a) {
+  fp4_status st = check_f8_product(x, w, n_experts, a.gated, true, what, a);
+  if (st != FP4_OK) return st;
+  const int64_t width = a.gated ? w->rows / 2 : w->rows;
+  if (y_kind != FP8_OUT_E4M3 &&
+      (st = check_rows(y, ldy, width, y_kind == FP4_IN_FP32 ? 4 : 2, x->rows > 0 && width > 0, what, "output")) != FP4_OK)
+    return st;
+  if (n_experts != 0 && (!offsets || !aligned(offsets, 4)))
+    return fail(FP4_EINVAL, "%s: offsets must be a 4-byte aligned pointer", what);
+  const size_t need = fp4k::f8_gemm_ws(a);
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 16)))
+    return fail(FP4_EINVAL, "%s: workspace of %zu bytes, %zu needed (16-byte aligned)", what, ws ? ws_bytes : (size_t)0,
+                need);
+  a.offsets = n_experts ? offsets : nullptr;
+  a.y = y;
+  a.y_kind = y_kind;
+  a.ldy = ldy;
+  a.ws = ws;
+  a.stream = (hipStream_t)stream;
+  return hip_status(fp4k::run_f8_gemm(a), what);
+}
+
+fp4_status check_act(int32_t act, const char* what) {
+  if (act < FP8_ACT_SILU || act > FP8_ACT_GELU_TANH) return fail(FP4_EINVAL, "%s: unknown activation %d", what, act);
+  return FP4_OK;
+}
+
+// What the two forms of the gated gradient share.
+fp4_status check_gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f, int64_t lddh, const void* gu,
+                            int64_t ldgu, int32_t act, const char* what, fp4k::GatedGradArgs& a) {
+  fp4_status st;
+  if ((st = check_io_dtype(dtype, what, "input")) != FP4_OK) return st;
+  if ((st = check_act(act, what)) != FP4_OK) return st;
+  if (rows < 0 || f < 0) return fail(FP4_EINVAL, "%s: negative size", what);
+  if (rows > MAX_SLOTS || f > MAX_SLOTS / 2) return fail(FP4_EUNSUPPORTED, "%s: rows below 2^31 and f below 2^30", what);
+  const int64_t esz = dtype == FP4_IN_FP32 ? 4 : 2;
+  const bool some = rows > 0 && f > 0;
+  if ((st = check_rows(dh, lddh, f, esz, some, what, "dh")) != FP4_OK) return st;
+  if ((st = check_rows(gu, ldgu, 2 * f, esz, some, what, "gu")) != FP4_OK) return st;
+  a.dh = dh;
+  a.gu = gu;
+  a.f32 = dtype == FP4_IN_FP32;
+  a.rows = rows;
+  a.f = f;
+  a.lddh = lddh;
+  a.ldgu = ldgu;
+  a.act = act;
+  return FP4_OK;
+}
+
+constexpr int64_t MAX_F8_TILES = int64_t(1) << 24;   // workgroups of 256 threads in a launch
 
 }  // namespace
 
@@ -803,6 +919,139 @@ fp4_status fp4_expert_linear(const void* x, int32_t x_dtype, int64_t rows, int64
   fp4_status st = check_experts(n_experts, what);
   if (st != FP4_OK) return st;
   return wlinear(x, x_dtype, rows, ldx, w, n_experts, offsets, y, y_dtype, ldy, ws, ws_bytes, stream, what);
+}
+
+fp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t view,
+                        int32_t scale, uint8_t* q, void* s, uint8_t* qt, void* st, void* stream) {
+  const char* what = "fp8_quantize";
+  fp4_status e;
+  if ((e = check_io_dtype(x_dtype, what, "input")) != FP4_OK) return e;
+  if ((e = check_f8_scale(scale, what)) != FP4_OK) return e;
+  if (view < FP4_VIEW_ROW || view > FP8_VIEW_ROWCOL) return fail(FP4_EINVAL, "%s: unknown view %d", what, view);
+  if (rows < 0 || cols < 0) return fail(FP4_EINVAL, "%s: negative size", what);
+  if (rows > MAX_SLOTS || cols > MAX_SLOTS) return fail(FP4_EUNSUPPORTED, "%s: rows and cols must be below 2^31", what);
+  if (((rows + 127) / 128) * ((cols + 127) / 128) >= MAX_F8_TILES)
+    return fail(FP4_EUNSUPPORTED, "%s: 2^24 tiles of 128 x 128 or more", what);
+  const bool some = rows > 0 && cols > 0;
+  if ((e = check_rows(x, ld, cols, x_dtype == FP4_IN_FP32 ? 4 : 2, some, what, "x")) != FP4_OK) return e;
+  if (some) {
+    if (view != FP4_VIEW_COL && (e = check_f8_out(q, s, scale, what, "row view")) != FP4_OK) return e;
+    if (view == FP4_VIEW_TILE2D && (e = check_f8_out(qt, s, scale, what, "transposed view")) != FP4_OK) return e;
+    if ((view == FP4_VIEW_COL || view == FP8_VIEW_ROWCOL) &&
+        (e = check_f8_out(qt, st, scale, what, "transposed view")) != FP4_OK)
+      return e;
+  }
+  fp4k::F8QuantArgs a{x, x_dtype == FP4_IN_FP32, rows, cols, ld, view, scale == FP8_SCALE_E8M0, q, s, qt, st,
+                      (hipStream_t)stream};
+  return hip_status(fp4k::run_f8_quantize(a), what);
+}
+
+fp4_status fp8_dequantize(const fp8_operand* o, void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+  const char* what = "fp8_dequantize";
+  fp4_status st;
+  if ((st = check_f8_operand(o, true, what, "operand")) != FP4_OK) return st;
+  if ((st = check_io_dtype(y_dtype, what, "output")) != FP4_OK) return st;
+  const bool f32 = y_dtype == FP4_IN_FP32;
+  if ((st = check_rows(y, ldy, o->k, f32 ? 4 : 2, o->rows > 0 && o->k > 0, what, "y")) != FP4_OK) return st;
+  return hip_status(fp4k::run_f8_dequantize(f8_operand(o), y, f32, ldy, (hipStream_t)stream), what);
+}
+
+fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
+                              size_t* ws_bytes) {
+  const char* what = "fp8_gemm_workspace";
+  if ((gated != 0 && gated != 1) || (f32 != 0 && f32 != 1)) return fail(FP4_EINVAL, "%s: gated and f32 must be 0 or 1", what);
+  if (!w) return fail(FP4_EINVAL, "%s: NULL weight", what);
+  if (!ws_bytes) return fail(FP4_EINVAL, "NULL size output");
+  const fp8_operand x{nullptr, nullptr, w->scale, FP4_SCALES_1D, rows, w->k};
+  fp4k::F8GemmArgs a{};
+  a.f32 = f32 != 0;
+  fp4_status st = check_f8_product(&x, w, n_experts, gated != 0, false, what, a);
+  if (st != FP4_OK) return st;
+  *ws_bytes = fp4k::f8_gemm_ws(a);
+  return ok();
+}
+
+fp4_status fp8_gemm(const fp8_operand* a, const fp8_operand* b, void* y, int32_t y_dtype, int64_t ldy, void* ws,
+                    size_t ws_bytes, void* stream) {
+  const char* what = "fp8_gemm";
+  fp4_status st = check_io_dtype(y_dtype, what, "output");
+  if (st != FP4_OK) return st;
+  fp4k::F8GemmArgs args{};
+  args.f32 = y_dtype == FP4_IN_FP32;
+  return f8_product(a, b, 0, nullptr, y, y_dtype, ldy, ws, ws_bytes, stream, what, args);
+}
+
+fp4_status fp8_expert_gemm(const fp8_operand* x, const fp8_operand* w, int32_t n_experts, const int32_t* offsets,
+                           void* y, int32_t y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  const char* what = "fp8_expert_gemm";
+  fp4_status st;
+  if ((st = check_io_dtype(y_dtype, what, "output")) != FP4_OK) return st;
+  if ((st = check_experts(n_experts, what)) != FP4_OK) return st;
+  fp4k::F8GemmArgs args{};
+  args.f32 = y_dtype == FP4_IN_FP32;
+  return f8_product(x, w, n_experts, offsets, y, y_dtype, ldy, ws, ws_bytes, stream, what, args);
+}
+
+fp4_status fp8_gated(const fp8_operand* x, const fp8_operand* w, int32_t n_experts, const int32_t* offsets,
+                     int32_t act, void* h, int32_t h_kind, int64_t ldh, void* hs, void* gu, int32_t gu_dtype,
+                     int64_t ldgu, void* ws, size_t ws_bytes, void* stream) {
+  const char* what = "fp8_gated";
+  fp4_status st;
+  if ((st = check_act(act, what)) != FP4_OK) return st;
+  if (h_kind != FP8_OUT_E4M3 && (st = check_io_dtype(h_kind, what, "output")) != FP4_OK) return st;
+  fp4k::F8GemmArgs a{};
+  a.gated = true;
+  a.act = act;
+  a.ys = hs;
+  a.f32 = h_kind == FP4_IN_FP32 || (gu && gu_dtype == FP4_IN_FP32);
+  if ((st = check_f8_product(x, w, n_experts, true, true, what, a)) != FP4_OK) return st;
+  const bool some = x->rows > 0 && w->rows > 0;
+  if (h_kind == FP8_OUT_E4M3 && some && (st = check_f8_out(h, hs, x->scale, what, "output")) != FP4_OK) return st;
+  if (gu) {
+    if ((st = check_io_dtype(gu_dtype, what, "gu")) != FP4_OK) return st;
+    if ((st = check_rows(gu, ldgu, w->rows, gu_dtype == FP4_IN_FP32 ? 4 : 2, some, what, "gu")) != FP4_OK) return st;
+    a.gu = gu;
+    a.gu_f32 = gu_dtype == FP4_IN_FP32;
+    a.ldgu = ldgu;
+  }
+  return f8_product(x, w, n_experts, offsets, h, h_kind, ldh, ws, ws_bytes, stream, what, a);
+}
+
+fp4_status gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f, int64_t lddh, const void* gu,
+                      int64_t ldgu, int32_t act, void* dgu, int64_t lddgu, void* stream) {
+  const char* what = "gated_grad";
+  fp4k::GatedGradArgs a{};
+  fp4_status st = check_gated_grad(dh, dtype, rows, f, lddh, gu, ldgu, act, what, a);
+  if (st != FP4_OK) return st;
+  if ((st = check_rows(dgu, lddgu, 2 * f, dtype == FP4_IN_FP32 ? 4 : 2, rows > 0 && f > 0, what, "dgu")) != FP4_OK) return st;
+  a.dgu = dgu;
+  a.lddgu = lddgu;
+  a.stream = (hipStream_t)stream;
+  return hip_status(fp4k::run_gated_grad(a), what);
+}
+
+fp4_status fp8_gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f, int64_t lddh, const void* gu,
+                          int64_t ldgu, int32_t act, int32_t scale, uint8_t* q, void* s, uint8_t* qt, void* st,
+                          void* stream) {
+  const char* what = "fp8_gated_grad";
+  fp4k::GatedGradArgs a{};
+  fp4_status e = check_gated_grad(dh, dtype, rows, f, lddh, gu, ldgu, act, what, a);
+  if (e != FP4_OK) return e;
+  if ((e = check_f8_scale(scale, what)) != FP4_OK) return e;
+  if (f % 128) return fail(FP4_EUNSUPPORTED, "%s: f must be a multiple of 128 (got %lld)", what, (long long)f);
+  if (((rows + 127) / 128) * (f / 128) >= MAX_F8_TILES) return fail(FP4_EUNSUPPORTED, "%s: 2^24 tiles or more", what);
+  if (!q && !qt) return fail(FP4_EINVAL, "%s: no view to write", what);
+  if (rows > 0 && f > 0) {
+    if (q && (e = check_f8_out(q, s, scale, what, "row view")) != FP4_OK) return e;
+    if (qt && (e = check_f8_out(qt, st, scale, what, "transposed view")) != FP4_OK) return e;
+  }
+  a.e8 = scale == FP8_SCALE_E8M0;
+  a.q = q;
+  a.s = s;
+  a.qt = qt;
+  a.st = st;
+  a.stream = (hipStream_t)stream;
+  return hip_status(fp4k::run_gated_grad(a), what);
 }
 
 }  // extern "C"
