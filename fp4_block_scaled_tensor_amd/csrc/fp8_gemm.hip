@@ -309,10 +309,13 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
     for (int i = 0; i < TN; ++i) read_w(0, i);
     read_x(0, 0, 0);
     int cur = 0;
-    for (int k = kc0; k < kc1; ++k) {
+    // One block; COPIES: the one after the next is copied into its buffer. (A branch inside would let the
+    // compiler sink the products behind it, away from the reads that feed them.)
+    auto block = [&](auto copies) {
       const int nxt = F::STAGE - cur;
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
         if (j == TM - 1) {
           // this wave's reads of the block are done and its copies of the next one have landed: behind the
           // barrier all waves' have (past the last block: unused reads of the other buffer)
@@ -341,10 +344,13 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
           }
           if (j == TM - 1) read_w(nxt, i);
         }
-        if (j == TM - 1 && k + 2 < kc1) copy(lds + cur);
+        if (j == TM - 1 && decltype(copies)::value) copy(lds + cur);
       }
       cur = nxt;
-    }
+    };
+    int k = kc0;
+    for (; k + 2 < kc1; ++k) block(std::true_type{});
+    for (; k < kc1; ++k) block(std::false_type{});
   }
 
   // Out: lane l of a product holds x row l % 16 and weight rows 4 (l / 16) + r. Each wave turns 16 rows of its
