@@ -37,6 +37,46 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
   return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
 }
 
+// The copies of lds_copy.hpp for all lanes (mask -1) or, without a branch, for none (0). Only
+// in code that all 64 lanes of a wave execute.
+__device__ __forceinline__ void lds_dma16_masked(const void* sbase, uint32_t voff, uint32_t dst, int mask) {
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_mov_b32 exec_lo, %3\n\t"
+      "s_mov_b32 exec_hi, %3\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %0, %1\n\t"
+      "s_mov_b64 exec, -1"
+      :
+      : "v"(voff), "s"(sbase), "s"(dst), "s"(mask)
+      : "memory", "m0");
+}
+template <bool BYTE>
+__device__ __forceinline__ void lds_dma_scale_masked(const void* sbase, uint32_t voff, uint32_t dst, int mask) {
+  if constexpr (BYTE)
+    asm volatile(
+        "s_mov_b32 m0, %2\n\t"
+        "s_mov_b32 exec_lo, %3\n\t"
+      "s_mov_b32 exec_hi, %3\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_ubyte %0, %1\n\t"
+        "s_mov_b64 exec, -1"
+        :
+        : "v"(voff), "s"(sbase), "s"(dst), "s"(mask)
+        : "memory", "m0");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %2\n\t"
+        "s_mov_b32 exec_lo, %3\n\t"
+      "s_mov_b32 exec_hi, %3\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %0, %1\n\t"
+        "s_mov_b64 exec, -1"
+        :
+        : "v"(voff), "s"(sbase), "s"(dst), "s"(mask)
+        : "memory", "m0");
+}
+
 enum : int { OUT_BF16 = 0, OUT_F32 = 1, OUT_F8 = 2 };
 // How a block's scales reach the sums: by the matrix core; as one float32 for 64 (gated: 32 and 32) of the
 // weight's rows; or as one for each of them. WIDE_*: the same for codes widened to bf16 (the products of
@@ -191,7 +231,8 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
     zero_tile<F>(p, m0, m1, c0, slice);
     return;
   }
-  const int kc0 = (int)((int64_t)p.kc * slice / p.slices), kc1 = (int)((int64_t)p.kc * (slice + 1) / p.slices);
+  const int kc0 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.kc * slice / p.slices));
+  const int kc1 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.kc * (slice + 1) / p.slices));
 
   // copies: a lane's 16 bytes of an 8-row piece (rows past the tensor read its last row; not stored)
   const int64_t width = GATED ? p.F : p.N;
@@ -229,24 +270,28 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
     }
   }
   const int64_t up = GATED ? p.F * p.kp : 0;
-  auto copy = [&](char* buf) {   // the next block
-#pragma unroll
-    for (int j = 0; j < F::XP; ++j) lds_dma16(xsrc, xoff[j], lds_offset(buf + (wave * F::XP + j) * 1024));
-#pragma unroll
-    for (int j = 0; j < F::WP; ++j) {
-      const int piece = wave * F::WP + j;
-      const char* src = GATED && (piece & 4) ? wsrc + up : wsrc;
-      lds_dma16(src, woff[j], lds_offset(buf + F::WROWS + piece * 1024));
-    }
-#pragma unroll
-    for (int j = 0; j < F::SP; ++j) {
+  // copy n of a wave's OPS of the next block; the last one moves on to the block after it
+  auto copy_op = [&](char* buf, int n, int mask) {
+    if (n < F::XP) {
+      lds_dma16_masked(xsrc, xoff[n], lds_offset(buf + (wave * F::XP + n) * 1024), mask);
+    } else if (n < F::XP + F::WP) {
+      const int piece = wave * F::WP + n - F::XP;
+      lds_dma16_masked(GATED && (piece & 4) ? wsrc + up : wsrc, woff[n - F::XP], lds_offset(buf + F::WROWS + piece * 1024),
+                       mask);
+    } else {
+      const int j = n - F::XP - F::WP;
       const uint32_t to = lds_offset(buf + F::SROWS + min(wave + j * NW, F::SCALES - 1) * 256);
-      if constexpr (SC == SC_E8 || SC == WIDE_E8) lds_dma1(ssrc[j], soff[j], to);
-      else lds_dma4(ssrc[j], soff[j], to);
+      lds_dma_scale_masked<SC == SC_E8 || SC == WIDE_E8>(ssrc[j], soff[j], to, mask);
       ssrc[j] += sstep[j];
     }
-    xsrc += ROWB;
-    wsrc += ROWB;
+    if (n == F::OPS - 1) {
+      xsrc += ROWB;
+      wsrc += ROWB;
+    }
+  };
+  auto copy = [&](char* buf) {
+#pragma unroll
+    for (int n = 0; n < F::OPS; ++n) copy_op(buf, n, -1);
   };
 
   v4f acc[TN][TM];
@@ -268,14 +313,25 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
     constexpr bool WIDE = SC == WIDE_E8 || SC == WIDE_F32;
     constexpr int WC = WIDE ? 4 : 1;   // products of a block
     using Frag = std::conditional_t<WIDE, v8bf, v8i>;
-    // A lane's pieces 2 kg and 2 kg + 1 of a row, as offsets of the wave's first row (rows 16 apart keep their
-    // pieces at the same places).
-    const int swz = (fr >> 1) & 7, p0 = (kg * 2 ^ swz) << 4, p1 = ((kg * 2 + 1) ^ swz) << 4;
-    const int xrow = (wm * TM * 16 + fr) * ROWB, wrow = F::WROWS + (wn * 64 + fr) * ROWB;
-    const int xsc = F::SROWS + (wm * TM * 16 + fr) * 4, wsc = F::SROWS + F::XS * 256 + wn * 256;
-    Frag wf[TN][WC], xf[2][WC];
-    uint32_t sx[2], swc[TN];   // SC_E8: swc
-    v4f swf[TN];               // else: the weight rows' scales (BAND: of the wave's first row, or of both halves')
+    // A lane's pieces kg and kg + 4 of a row, as offsets of the wave's first row (rows 16 apart keep their pieces
+    // at the same places). The order of k inside a block is free as long as both operands agree; with pieces
+    // 2 kg and 2 kg + 1 the lanes that the LDS serves together met in its banks (43% of its cycles).
+    const int p0 = (kg ^ ((fr >> 1) & 7)) << 4, p1 = p0 ^ 64;
+    // In each of the two buffers; the rows of a wave are a constant apart. (Opaque, or the compiler keeps a
+    // register for each row of either buffer.)
+    int xat[2][2], wat[2][2], xsat[2], wsat[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int x = b * F::STAGE + (wm * TM * 16 + fr) * ROWB, w = b * F::STAGE + F::WROWS + (wn * 64 + fr) * ROWB;
+      xat[b][0] = x + p0, xat[b][1] = x + p1, wat[b][0] = w + p0, wat[b][1] = w + p1;
+      xsat[b] = b * F::STAGE + F::SROWS + (wm * TM * 16 + fr) * 4;
+      wsat[b] = b * F::STAGE + F::SROWS + F::XS * 256 + wn * 256 + (SC == SC_E8 ? fr * 4 : SC == SC_F32_BAND ? 0 : kg * 16);
+      asm("" : "+v"(xat[b][0]), "+v"(xat[b][1]), "+v"(wat[b][0]), "+v"(wat[b][1]), "+v"(xsat[b]), "+v"(wsat[b]));
+    }
+    // the weight rows' fragments and scales of this block and, from its last products on, of the next
+    Frag wf[2][TN][WC], xf[2][WC];
+    uint32_t sx[2], swc[2][TN];   // SC_E8: swc
+    v4f swf[2][TN];               // else (BAND: of the wave's first row, or of both halves')
     auto take = [&](Frag* to, int at0, int at1) {
       const v8i c = read_row(lds, at0, at1);
       if constexpr (WIDE) {
@@ -285,72 +341,91 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
         to[0] = c;
       }
     };
-    auto read_w = [&](int buf, int i) {
-      take(wf[i], buf + wrow + i * 16 * ROWB + p0, buf + wrow + i * 16 * ROWB + p1);
-      const char* s = lds + buf + wsc + i * 64;
+    auto read_w = [&](int b, int i) {   // buffer b's, which are wf[b] and its scales
+      take(wf[b][i], wat[b][0] + i * 16 * ROWB, wat[b][1] + i * 16 * ROWB);
+      const char* s = lds + wsat[b] + i * 64;
       if constexpr (SC == SC_E8) {
-        swc[i] = *reinterpret_cast<const uint32_t*>(s + fr * 4);
+        swc[b][i] = *reinterpret_cast<const uint32_t*>(s);
       } else if constexpr (SC == SC_F32_BAND) {
-        swf[i][0] = *reinterpret_cast<const float*>(s);
+        swf[b][i][0] = *reinterpret_cast<const float*>(s);
       } else {
-        swf[i] = *reinterpret_cast<const v4f*>(s + kg * 16);
+        swf[b][i] = *reinterpret_cast<const v4f*>(s);
         if constexpr (SC == WIDE_E8) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) swf[i][r] = e8m0_value(__float_as_uint(swf[i][r]));
+          for (int r = 0; r < 4; ++r) swf[b][i][r] = e8m0_value(__float_as_uint(swf[b][i][r]));
         }
       }
     };
-    auto read_x = [&](int buf, int j, int to) {
-      take(xf[to], buf + xrow + j * 16 * ROWB + p0, buf + xrow + j * 16 * ROWB + p1);
-      sx[to] = *reinterpret_cast<const uint32_t*>(lds + buf + xsc + j * 64);
+    auto read_x = [&](int b, int j, int to) {
+      take(xf[to], xat[b][0] + j * 16 * ROWB, xat[b][1] + j * 16 * ROWB);
+      sx[to] = *reinterpret_cast<const uint32_t*>(lds + xsat[b] + j * 64);
       if constexpr (SC == WIDE_E8) sx[to] = __float_as_uint(e8m0_value(sx[to]));
     };
 #pragma unroll
     for (int i = 0; i < TN; ++i) read_w(0, i);
     read_x(0, 0, 0);
-    int cur = 0;
-    // One block; COPIES: the one after the next is copied into its buffer. (A branch inside would let the
-    // compiler sink the products behind it, away from the reads that feed them.)
-    auto block = [&](auto copies) {
-      const int nxt = F::STAGE - cur;
+    // A block's products, x rows (groups j) outermost. Fragments of x are read one group ahead. The barrier stands
+    // in the middle of the last group but one: by then this wave has read all of the block and its copies of the
+    // next one have landed, so the next block's first fragments load under the six products left, and the
+    // copies into the freed buffer are dealt out between them. Float32 scales: a product's sums are taken one
+    // product later, so that it is done by then.
+    // (A branch around the copies would let the compiler sink the products behind it, away from their reads:
+    // hence the mask.)
+    constexpr int SLOTS = TN + TN / 2;
+    v4f held[2] = {};
+    v4f hscale[2] = {};
+    auto block = [&](auto parity, int copies) {
+      constexpr int W = decltype(parity)::value;   // its buffer
 #pragma unroll
-      for (int j = 0; j < TM; ++j) {
+      for (int n = 0; n < TM * TN; ++n) {
+        const int j = n / TN, i = n % TN, slot = n - (TM * TN - SLOTS);
         __builtin_amdgcn_sched_barrier(0);
-        if (j == TM - 1) {
-          // this wave's reads of the block are done and its copies of the next one have landed: behind the
-          // barrier all waves' have (past the last block: unused reads of the other buffer)
+        if (i == 0 && j + 1 < TM) read_x(W, j + 1, (j + 1) & 1);
+        if (slot == 0) {
+          // (past the last block: unused reads of the other buffer)
           wait_copies();
           __syncthreads();
-          read_x(nxt, 0, 0);
+        }
+        if constexpr (SC == SC_E8) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[W][i][0], xf[j & 1][0], acc[i][j], 0, 0, 0,
+                                                                       (int)swc[W][i], 0, (int)sx[j & 1]);
         } else {
-          read_x(cur, j + 1, (j + 1) & 1);
-        }
+          v4f t = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < TN; ++i) {
-          if constexpr (SC == SC_E8) {
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i][0], xf[j & 1][0], acc[i][j], 0, 0, 0,
-                                                                         (int)swc[i], 0, (int)sx[j & 1]);
-          } else {
-            v4f t = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int q = 0; q < WC; ++q) {
-              if constexpr (WIDE) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i][q], xf[j & 1][q], t, 0, 0, 0);
-              else t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i][q], xf[j & 1][q], t, 0, 0, 0, 0x7F, 0, 0x7F);
-            }
-            const float sxf = __uint_as_float(sx[j & 1]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[i][j][r] = __builtin_fmaf(t[r], sxf * swf[i][SC == SC_F32_BAND ? 0 : r], acc[i][j][r]);
+          for (int q = 0; q < WC; ++q) {
+            if constexpr (WIDE) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[W][i][q], xf[j & 1][q], t, 0, 0, 0);
+            else t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[W][i][q], xf[j & 1][q], t, 0, 0, 0, 0x7F, 0, 0x7F);
           }
-          if (j == TM - 1) read_w(nxt, i);
+          held[n & 1] = t;
+          const float sxf = __uint_as_float(sx[j & 1]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) hscale[n & 1][r] = sxf * swf[W][i][SC == SC_F32_BAND ? 0 : r];
+          const int b = (n + TM * TN - 1) % (TM * TN), bi = b % TN, bj = b / TN;   // the product before
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[bi][bj][r] = __builtin_fmaf(held[b & 1][r], hscale[b & 1][r], acc[bi][bj][r]);
         }
-        if (j == TM - 1 && decltype(copies)::value) copy(lds + cur);
+        if (slot >= 0) {
+          if (slot < TN) read_w(1 - W, slot);
+          else if (slot == TN) read_x(1 - W, 0, 0);
+#pragma unroll
+          for (int o = F::OPS * slot / SLOTS; o < F::OPS * (slot + 1) / SLOTS; ++o) copy_op(lds + W * F::STAGE, o, copies);
+        }
       }
-      cur = nxt;
     };
+    const std::integral_constant<int, 0> even{};
+    const std::integral_constant<int, 1> odd{};
     int k = kc0;
-    for (; k + 2 < kc1; ++k) block(std::true_type{});
-    for (; k < kc1; ++k) block(std::false_type{});
+    for (; k + 1 < kc1; k += 2) {
+      block(even, __builtin_amdgcn_readfirstlane(k + 2 < kc1 ? -1 : 0));
+      block(odd, __builtin_amdgcn_readfirstlane(k + 3 < kc1 ? -1 : 0));
+    }
+    if (k < kc1) block(even, 0);
+    if constexpr (SC != SC_E8) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[TN - 1][TM - 1][r] = __builtin_fmaf(held[(TM * TN - 1) & 1][r], hscale[(TM * TN - 1) & 1][r], acc[TN - 1][TM - 1][r]);
+    }
   }
 
   // Out: lane l of a product holds x row l % 16 and weight rows 4 (l / 16) + r. Each wave turns 16 rows of its
