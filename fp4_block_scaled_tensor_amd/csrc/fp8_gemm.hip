@@ -100,7 +100,7 @@ struct F8Params {
   char* gu;                  // the gated projections, or null
   int64_t ldgu;
   int out;                   // OUT_*
-  bool gu_f32, y_vec, gu_vec;   // vec: rows take 4-element stores
+  bool gu_f32, y_vec, gu_vec;   // vec: rows take 16-byte stores
   uint32_t mtiles, ntiles;   // mtiles: an upper bound with offsets
   int slices;                // parts of K, each with its own rows in `part`
   float* part;               // [slices][rows][N] sums of a split K, or null
@@ -137,21 +137,22 @@ __device__ __forceinline__ F8Scale hs_scale(const F8Params& p, uint32_t amax) {
 // K, and their scales, are copied straight into LDS, two blocks deep. Row r (128 bytes) keeps its 16-byte
 // piece j at j ^ ((r >> 1) & 7), so that 16 rows reading one piece fall on all banks.
 constexpr int ROWB = F8_BLOCK;
-constexpr int BN = 256, WN = 4, TN = 4;   // weight rows of a tile, waves across them, 16-row groups of a wave
+constexpr int BN = 256;   // weight rows of a tile
 
-template <int TM_, int WM_, int SC_, bool GATED_>
+template <int TM_, int WM_, int SC_, bool GATED_, int WN_ = 4>
 struct TileForm {
-  static constexpr int TM = TM_, WM = WM_, SC = SC_, NW = WM * WN, BM = 16 * TM * WM;
+  static constexpr int TM = TM_, WM = WM_, SC = SC_, WN = WN_, NW = WM * WN, BM = 16 * TM * WM;
+  static constexpr int TN = BN / 16 / WN, CW = TN * 16;                 // 16-row groups and weight rows of a wave
   static constexpr bool GATED = GATED_;
   static constexpr int XP = BM / 8 / NW, WP = BN / 8 / NW;              // copies of 8 rows, a wave's
   static constexpr int XS = (BM + 63) / 64, SCALES = XS + BN / 64;      // copies of 64 scales, all
   static constexpr int SP = (SCALES + NW - 1) / NW;
   static constexpr int OPS = XP + WP + SP;                              // a wave's copies of one block
-  static constexpr int WROWS = BM * ROWB, SROWS = (BM + BN) * ROWB, STAGE = SROWS + SCALES * 256;
-  static constexpr int OLD = TN * 16 + 4;                               // a wave's output row, padded by 16 bytes
+  // LDS: x rows of both buffers, weight rows of both, scales of both (x, then weight)
+  static constexpr int XBUF = BM * ROWB, WBUF = BN * ROWB, SBUF = SCALES * 256, WROWS = 2 * XBUF, SROWS = WROWS + 2 * WBUF;
   static constexpr int CODES = BM * F8_BLOCK;                           // h's codes, then its row maxima
-  static constexpr int LDS = 2 * STAGE;
-  static_assert(NW * 16 * OLD * 4 <= LDS && CODES + WN * BM * 4 <= LDS, "the outputs fit the buffers");
+  static constexpr int LDS = SROWS + 2 * SBUF;
+  static_assert(CODES + WN * BM * 4 <= LDS, "the outputs fit the buffers");
   static_assert(TM % 2 == 0 && BM % (8 * NW) == 0, "");
 };
 
@@ -173,6 +174,67 @@ __device__ __forceinline__ v8bf widen8(int lo, int hi) {
 // The value of an E8M0 code: 2^(c - 127), NaN for 255.
 __device__ __forceinline__ float e8m0_value(uint32_t c) {
   return __uint_as_float(c == 0 ? 1u << 22 : c == 255 ? 0x7FC00000u : c << 23);
+}
+
+// Columns i < NI of a wave's products (16 to a product) to rows of y, as float32 or rounded to bf16: as many of
+// its rows at a time as its share of the LDS holds, turned there so that lanes store 16 bytes of whole rows.
+// Columns from `half` of the NI on (gated: the up projection's) go `up` further on; 0: one run of columns.
+// Piece j (16 bytes) of row r stays at j ^ (r & 7) of its eight.
+template <class F, bool F32, int NI>
+__device__ __forceinline__ void store_wave(char* lds, const v4f (&acc)[F::TN][F::TM], char* y, int64_t ld, bool vec,
+                                           int64_t m0, int64_t m1, int64_t c0, int64_t width, int64_t up) {
+  constexpr int E = F32 ? 4 : 2, COLS = NI * 16, RB = COLS * E, PIECES = RB / 16, PER = 16 / E, SW = PIECES < 8 ? PIECES - 1 : 7;
+  constexpr int SHARE = F::LDS / F::NW / 256 * 256;   // the same for every call: waves may be in different ones
+  constexpr int FIT = SHARE / (16 * RB), JP = FIT >= F::TM ? F::TM : FIT >= 4 ? 4 : FIT >= 2 ? 2 : 1;
+  static_assert(FIT >= 1 && F::TM % JP == 0, "");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), fr = lane & 15, kg = lane >> 4;
+  char* mine = lds + wave * SHARE;
+  const int half = up ? COLS / 2 : COLS;
+#pragma unroll
+  for (int j0 = 0; j0 < F::TM; j0 += JP) {
+#pragma unroll
+    for (int j = 0; j < JP; ++j)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = j * 16 + fr, at = (i * 16 + kg * 4) * E;
+        const v4f v = acc[i][j0 + j];
+        char* to = mine + r * RB + (((at >> 4) ^ (r & SW)) << 4) + (at & 15);
+        if constexpr (F32) *reinterpret_cast<v4f*>(to) = v;
+        else *reinterpret_cast<uint2*>(to) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      }
+    wave_order();
+    if (vec) {
+#pragma unroll 8
+      for (int o = lane; o < JP * 16 * PIECES; o += 64) {
+        const int r = o / PIECES, piece = o % PIECES, c = piece * PER, in = c >= half ? c - half : c;
+        const uint4 v = *reinterpret_cast<const uint4*>(mine + r * RB + ((piece ^ (r & SW)) << 4));
+        const int64_t m = m0 + j0 * 16 + r;
+        if (m >= m1 || c0 + in >= width) continue;
+        char* to = y + (m * ld + c0 + in + (c >= half ? up : 0)) * E;
+        if (c0 + in + PER <= width) {
+          *reinterpret_cast<uint4*>(to) = v;
+        } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int q = 0; q < (int)(width - c0) - in; ++q) {
+            if constexpr (F32) reinterpret_cast<uint32_t*>(to)[q] = w[q];
+            else reinterpret_cast<uint16_t*>(to)[q] = (uint16_t)(w[q >> 1] >> (16 * (q & 1)));
+          }
+        }
+      }
+    } else {
+#pragma unroll 4
+      for (int o = lane; o < JP * 16 * COLS; o += 64) {
+        const int r = o / COLS, c = o % COLS, in = c >= half ? c - half : c, at = c * E;
+        const char* from = mine + r * RB + (((at >> 4) ^ (r & SW)) << 4) + (at & 15);
+        const int64_t m = m0 + j0 * 16 + r;
+        if (m >= m1 || c0 + in >= width) continue;
+        const int64_t to = m * ld + c0 + in + (c >= half ? up : 0);
+        if constexpr (F32) reinterpret_cast<uint32_t*>(y)[to] = *reinterpret_cast<const uint32_t*>(from);
+        else reinterpret_cast<uint16_t*>(y)[to] = *reinterpret_cast<const uint16_t*>(from);
+      }
+    }
+    wave_order();
+  }
 }
 
 // h of dropped rows, or of a tile's rows, as zeros
@@ -206,8 +268,8 @@ __device__ __forceinline__ void zero_tile(const F8Params& p, int64_t m0, int64_t
 }
 
 template <class F, int ACT>
-__global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
-  constexpr int TM = F::TM, NW = F::NW, BM = F::BM, SC = F::SC;
+__global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_tile(F8Params p) {
+  constexpr int TM = F::TM, TN = F::TN, WN = F::WN, CW = F::CW, NW = F::NW, BM = F::BM, SC = F::SC;
   constexpr bool GATED = F::GATED;
   __shared__ __attribute__((aligned(1024))) char lds[F::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -244,8 +306,8 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
     const int r = (wave * F::XP + j) * 8 + (lane >> 3);
     xoff[j] = (uint32_t)(min((int64_t)r, m1 - 1 - m0) * p.kp) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
   }
-  // row r of the tile's weight rows: column c0 + r, or of each wave's 64 the first 32 features' gate and up
-  auto column = [&](int r) { return min((int64_t)(GATED ? (r >> 6) * 32 + (r & 31) : r), width - 1 - c0); };
+  // row r of the tile's weight rows: column c0 + r, or of each wave's CW the CW / 2 features' gate and up
+  auto column = [&](int r) { return min((int64_t)(GATED ? r / CW * (CW / 2) + r % (CW / 2) : r), width - 1 - c0); };
 #pragma unroll
   for (int j = 0; j < F::WP; ++j) {
     const int r = (wave * F::WP + j) * 8 + (lane >> 3);
@@ -263,7 +325,7 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
       ssrc[j] = uniform_ptr(p.xs + (m0 * p.kc + kc0) * p.es);
       sstep[j] = p.es;
     } else {
-      const int64_t row = c0 + column(r) + (GATED && (r & 32) ? p.F : 0);
+      const int64_t row = c0 + column(r) + (GATED && (r & (CW / 2)) ? p.F : 0);
       soff[j] = (uint32_t)((row >> p.ws_band) * p.ws_row * p.es);
       ssrc[j] = uniform_ptr(p.ws + (int64_t)e * p.ws_stride + (int64_t)kc0 * p.ws_k * p.es);
       sstep[j] = p.ws_k * p.es;
@@ -271,16 +333,16 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
   }
   const int64_t up = GATED ? p.F * p.kp : 0;
   // copy n of a wave's OPS of the next block; the last one moves on to the block after it
-  auto copy_op = [&](char* buf, int n, int mask) {
+  auto copy_op = [&](int b, int n, int mask) {
     if (n < F::XP) {
-      lds_dma16_masked(xsrc, xoff[n], lds_offset(buf + (wave * F::XP + n) * 1024), mask);
+      lds_dma16_masked(xsrc, xoff[n], lds_offset(lds + b * F::XBUF + (wave * F::XP + n) * 1024), mask);
     } else if (n < F::XP + F::WP) {
       const int piece = wave * F::WP + n - F::XP;
-      lds_dma16_masked(GATED && (piece & 4) ? wsrc + up : wsrc, woff[n - F::XP], lds_offset(buf + F::WROWS + piece * 1024),
+      lds_dma16_masked(GATED && (piece & (CW / 16)) ? wsrc + up : wsrc, woff[n - F::XP], lds_offset(lds + F::WROWS + b * F::WBUF + piece * 1024),
                        mask);
     } else {
       const int j = n - F::XP - F::WP;
-      const uint32_t to = lds_offset(buf + F::SROWS + min(wave + j * NW, F::SCALES - 1) * 256);
+      const uint32_t to = lds_offset(lds + F::SROWS + b * F::SBUF + min(wave + j * NW, F::SCALES - 1) * 256);
       lds_dma_scale_masked<SC == SC_E8 || SC == WIDE_E8>(ssrc[j], soff[j], to, mask);
       ssrc[j] += sstep[j];
     }
@@ -289,9 +351,9 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
       wsrc += ROWB;
     }
   };
-  auto copy = [&](char* buf) {
+  auto copy = [&](int b) {
 #pragma unroll
-    for (int n = 0; n < F::OPS; ++n) copy_op(buf, n, -1);
+    for (int n = 0; n < F::OPS; ++n) copy_op(b, n, -1);
   };
 
   v4f acc[TN][TM];
@@ -302,9 +364,9 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
 
   const int fr = lane & 15, kg = lane >> 4;
   if (kc0 < kc1) {
-    copy(lds);
+    copy(0);
     if (kc0 + 1 < kc1) {
-      copy(lds + F::STAGE);
+      copy(1);
       wait_all_but<F::OPS>();
     } else {
       wait_all_but<0>();
@@ -317,17 +379,12 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
     // at the same places). The order of k inside a block is free as long as both operands agree; with pieces
     // 2 kg and 2 kg + 1 the lanes that the LDS serves together met in its banks (43% of its cycles).
     const int p0 = (kg ^ ((fr >> 1) & 7)) << 4, p1 = p0 ^ 64;
-    // In each of the two buffers; the rows of a wave are a constant apart. (Opaque, or the compiler keeps a
-    // register for each row of either buffer.)
-    int xat[2][2], wat[2][2], xsat[2], wsat[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int x = b * F::STAGE + (wm * TM * 16 + fr) * ROWB, w = b * F::STAGE + F::WROWS + (wn * 64 + fr) * ROWB;
-      xat[b][0] = x + p0, xat[b][1] = x + p1, wat[b][0] = w + p0, wat[b][1] = w + p1;
-      xsat[b] = b * F::STAGE + F::SROWS + (wm * TM * 16 + fr) * 4;
-      wsat[b] = b * F::STAGE + F::SROWS + F::XS * 256 + wn * 256 + (SC == SC_E8 ? fr * 4 : SC == SC_F32_BAND ? 0 : kg * 16);
-      asm("" : "+v"(xat[b][0]), "+v"(xat[b][1]), "+v"(wat[b][0]), "+v"(wat[b][1]), "+v"(xsat[b]), "+v"(wsat[b]));
-    }
+    // Rows of a wave and the two buffers are constants apart. (Opaque, or the compiler keeps a register for each.)
+    int xat[2], wat[2], xsat = F::SROWS + (wm * TM * 16 + fr) * 4;
+    int wsat = F::SROWS + F::XS * 256 + wn * CW * 4 + (SC == SC_E8 ? fr * 4 : SC == SC_F32_BAND ? 0 : kg * 16);
+    xat[0] = (wm * TM * 16 + fr) * ROWB + p0, xat[1] = xat[0] - p0 + p1;
+    wat[0] = F::WROWS + (wn * CW + fr) * ROWB + p0, wat[1] = wat[0] - p0 + p1;
+    asm("" : "+v"(xat[0]), "+v"(xat[1]), "+v"(wat[0]), "+v"(wat[1]), "+v"(xsat), "+v"(wsat));
     // the weight rows' fragments and scales of this block and, from its last products on, of the next
     Frag wf[2][TN][WC], xf[2][WC];
     uint32_t sx[2], swc[2][TN];   // SC_E8: swc
@@ -342,8 +399,8 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
       }
     };
     auto read_w = [&](int b, int i) {   // buffer b's, which are wf[b] and its scales
-      take(wf[b][i], wat[b][0] + i * 16 * ROWB, wat[b][1] + i * 16 * ROWB);
-      const char* s = lds + wsat[b] + i * 64;
+      take(wf[b][i], wat[0] + b * F::WBUF + i * 16 * ROWB, wat[1] + b * F::WBUF + i * 16 * ROWB);
+      const char* s = lds + wsat + b * F::SBUF + i * 64;
       if constexpr (SC == SC_E8) {
         swc[b][i] = *reinterpret_cast<const uint32_t*>(s);
       } else if constexpr (SC == SC_F32_BAND) {
@@ -357,8 +414,8 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
       }
     };
     auto read_x = [&](int b, int j, int to) {
-      take(xf[to], xat[b][0] + j * 16 * ROWB, xat[b][1] + j * 16 * ROWB);
-      sx[to] = *reinterpret_cast<const uint32_t*>(lds + xsat[b] + j * 64);
+      take(xf[to], xat[0] + b * F::XBUF + j * 16 * ROWB, xat[1] + b * F::XBUF + j * 16 * ROWB);
+      sx[to] = *reinterpret_cast<const uint32_t*>(lds + xsat + b * F::SBUF + j * 64);
       if constexpr (SC == WIDE_E8) sx[to] = __float_as_uint(e8m0_value(sx[to]));
     };
 #pragma unroll
@@ -409,7 +466,7 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
           if (slot < TN) read_w(1 - W, slot);
           else if (slot == TN) read_x(1 - W, 0, 0);
 #pragma unroll
-          for (int o = F::OPS * slot / SLOTS; o < F::OPS * (slot + 1) / SLOTS; ++o) copy_op(lds + W * F::STAGE, o, copies);
+          for (int o = F::OPS * slot / SLOTS; o < F::OPS * (slot + 1) / SLOTS; ++o) copy_op(W, o, copies);
         }
       }
     };
@@ -428,70 +485,43 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
     }
   }
 
-  // Out: lane l of a product holds x row l % 16 and weight rows 4 (l / 16) + r. Each wave turns 16 rows of its
-  // columns at a time through its own LDS rows.
-  float* turn = reinterpret_cast<float*>(lds) + wave * 16 * F::OLD;
-  const int64_t wrow0 = m0 + wm * TM * 16;
-  char* wide = p.part ? reinterpret_cast<char*>(p.part + (int64_t)slice * p.rows * p.N) : GATED ? p.gu : p.y;
-  const int64_t ldw = p.part ? p.N : GATED ? p.ldgu : p.ldy;
-  const bool wide_f32 = p.part || (GATED ? p.gu_f32 : p.out == OUT_F32);
-  const bool wide_vec = p.part ? p.N % 4 == 0 && p.F % 4 == 0 : GATED ? p.gu_vec : p.y_vec;
+  // Out: lane l of a product holds x row l % 16 and weight rows 4 (l / 16) + r. Each wave turns its columns
+  // through LDS rows of its own.
+  const int64_t wrow0 = m0 + wm * TM * 16, f0 = c0 + wn * (GATED ? CW / 2 : CW);
   __syncthreads();
+  if (p.part) store_wave<F, true, TN>(lds, acc, reinterpret_cast<char*>(p.part + (int64_t)slice * p.rows * p.N), p.N,
+                                      p.N % 4 == 0 && p.F % 4 == 0, wrow0, m1, f0, width, p.F);
+  else if constexpr (!GATED) {
+    if (p.out == OUT_F32) store_wave<F, true, TN>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
+    else store_wave<F, false, TN>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
+  } else {
+    if (p.gu && p.gu_f32) store_wave<F, true, TN>(lds, acc, p.gu, p.ldgu, p.gu_vec, wrow0, m1, f0, width, p.F);
+    else if (p.gu) store_wave<F, false, TN>(lds, acc, p.gu, p.ldgu, p.gu_vec, wrow0, m1, f0, width, p.F);
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    if (wide) {   // the columns themselves
+    for (int j = 0; j < TM; ++j)
 #pragma unroll
-      for (int i = 0; i < TN; ++i) *reinterpret_cast<v4f*>(turn + fr * F::OLD + i * 16 + kg * 4) = acc[i][j];
-      wave_order();
+      for (int i = 0; i < TN / 2; ++i)
 #pragma unroll
-      for (int o = 0; o < 4; ++o) {
-        const int r = o * 4 + kg, c = fr * 4;
-        const v4f v = *reinterpret_cast<const v4f*>(turn + r * F::OLD + c);
-        const int64_t m = wrow0 + j * 16 + r, col = c0 + (GATED ? wn * 32 + (c & 31) : wn * 64 + c);
-        if (m < m1 && col < width)
-          store4(wide, wide_f32, wide_vec, m * ldw + col + (GATED && c >= 32 ? p.F : 0), (int)min(width - col, (int64_t)4), v);
-      }
-      wave_order();
-    }
-    if constexpr (GATED) {
-      if (!p.part) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float g = acc[i][j][r];
-            acc[i][j][r] = g * act_gate<ACT>(g) * acc[i + 2][j][r];
-          }
-        if (p.out != OUT_F8) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) *reinterpret_cast<v4f*>(turn + fr * F::OLD + i * 16 + kg * 4) = acc[i][j];
-          wave_order();
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const int r = o * 8 + (lane >> 3), c = (lane & 7) * 4;
-            const v4f v = *reinterpret_cast<const v4f*>(turn + r * F::OLD + c);
-            const int64_t m = wrow0 + j * 16 + r, col = c0 + wn * 32 + c;
-            if (m < m1 && col < width)
-              store4(p.y, p.out == OUT_F32, p.y_vec, m * p.ldy + col, (int)min(width - col, (int64_t)4), v);
-          }
-          wave_order();
+        for (int r = 0; r < 4; ++r) {
+          const float g = acc[i][j][r];
+          acc[i][j][r] = g * act_gate<ACT>(g) * acc[i + TN / 2][j][r];
         }
-      }
-    }
+    if (p.out == OUT_F32) store_wave<F, true, TN / 2>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
+    else if (p.out == OUT_BF16) store_wave<F, false, TN / 2>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
   }
   if constexpr (GATED) {
     if (p.part || p.out != OUT_F8) return;
-    // h as codes: the four waves across hold the 128 features of a row's block
+    // h as codes: the waves across hold the 128 features of a row's block
     uint32_t* red = reinterpret_cast<uint32_t*>(lds + F::CODES);   // [WN][BM]
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       uint32_t a = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < TN / 2; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if (c0 + wn * 32 + i * 16 + kg * 4 + r >= width) acc[i][j][r] = 0.0f;
+          if (c0 + wn * (CW / 2) + i * 16 + kg * 4 + r >= width) acc[i][j][r] = 0.0f;
           a = max(a, mag_bits(acc[i][j][r]));
         }
       a = max(a, (uint32_t)__shfl_xor((int)a, 16, 64));
@@ -502,11 +532,14 @@ __global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       const int row = (wm * TM + j) * 16 + fr;
-      const F8Scale s = hs_scale(p, max(max(red[row], red[BM + row]), max(red[2 * BM + row], red[3 * BM + row])));
+      uint32_t a = red[row];
+#pragma unroll
+      for (int w = 1; w < WN; ++w) a = max(a, red[w * BM + row]);
+      const F8Scale s = hs_scale(p, a);
       if (wn == 0 && kg == 0 && m0 + row < m1) store_hs(p, m0 + row, c0 / F8_BLOCK, s.code);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<uint32_t*>(lds + row * F8_BLOCK + wn * 32 + i * 16 + kg * 4) =
+      for (int i = 0; i < TN / 2; ++i)
+        *reinterpret_cast<uint32_t*>(lds + row * F8_BLOCK + wn * (CW / 2) + i * 16 + kg * 4) =
             f8_pack4(acc[i][j][0] * s.enc, acc[i][j][1] * s.enc, acc[i][j][2] * s.enc, acc[i][j][3] * s.enc);
     }
     __syncthreads();
@@ -678,10 +711,10 @@ hipError_t run_f8_gemm(const F8GemmArgs& a) {
   p.ldgu = a.ldgu;
   p.gu_f32 = a.gu_f32;
   auto vec = [](const void* q, int64_t ld, bool f32) {
-    return ld % 4 == 0 && reinterpret_cast<uintptr_t>(q) % (f32 ? 16 : 8) == 0;
+    return ld % (f32 ? 4 : 8) == 0 && reinterpret_cast<uintptr_t>(q) % 16 == 0;
   };
   p.y_vec = a.y_kind != OUT_F8 && vec(a.y, a.ldy, a.y_kind == OUT_F32);
-  p.gu_vec = a.gu && vec(a.gu, a.ldgu, a.gu_f32) && p.F % 4 == 0;
+  p.gu_vec = a.gu && vec(a.gu, a.ldgu, a.gu_f32) && p.F % (a.gu_f32 ? 4 : 8) == 0;
   const TilePlan t = plan_tiles(a);
   p.mtiles = (uint32_t)t.mt;
   p.ntiles = (uint32_t)t.nt;
