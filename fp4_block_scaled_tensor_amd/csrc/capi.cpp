@@ -930,6 +930,7 @@ fp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t co
   if (view < FP4_VIEW_ROW || view > FP8_VIEW_ROWCOL) return fail(FP4_EINVAL, "%s: unknown view %d", what, view);
   if (rows < 0 || cols < 0) return fail(FP4_EINVAL, "%s: negative size", what);
   if (rows > MAX_SLOTS || cols > MAX_SLOTS) return fail(FP4_EUNSUPPORTED, "%s: rows and cols must be below 2^31", what);
+  if (ld > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: ld must be at most 2^22", what);
   if (((rows + 127) / 128) * ((cols + 127) / 128) >= MAX_F8_TILES)
     return fail(FP4_EUNSUPPORTED, "%s: 2^24 tiles of 128 x 128 or more", what);
   const bool some = rows > 0 && cols > 0;
@@ -1039,6 +1040,7 @@ fp4_status fp8_gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f
   if (e != FP4_OK) return e;
   if ((e = check_f8_scale(scale, what)) != FP4_OK) return e;
   if (f % 128) return fail(FP4_EUNSUPPORTED, "%s: f must be a multiple of 128 (got %lld)", what, (long long)f);
+  if (lddh > MAX_WIDTH || ldgu > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: lddh and ldgu must be at most 2^22", what);
   if (((rows + 127) / 128) * (f / 128) >= MAX_F8_TILES) return fail(FP4_EUNSUPPORTED, "%s: 2^24 tiles or more", what);
   if (!q && !qt) return fail(FP4_EINVAL, "%s: no view to write", what);
   if (rows > 0 && f > 0) {

@@ -114,19 +114,42 @@ __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v
 // sigmoid(x) = 1 / (1 + e^-x) by the hardware's exponential and reciprocal (each within an ulp or two)
 __device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
-// p with act(g) = g p: the sigmoid, the normal distribution's, or the sigmoid of its tanh form,
+// The normal distribution's P(g) and density d: with x = |g| / sqrt 2, erfc(x) = (a1 t + .. + a5 t^5) e^-x^2,
+// t = 1 / (1 + a0 x), within 1.5e-7 (Abramowitz and Stegun 7.1.26; Hastings, "Approximations for Digital
+// Computers"). The exponential serves the density too.
+__device__ __forceinline__ void normal_f32(float g, float& p, float& d) {
+  const float x = fabsf(g) * 0.70710678118654752f, e = __expf(-x * x);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+  float s = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+  s = __builtin_fmaf(s, t, 1.421413741f);
+  s = __builtin_fmaf(s, t, -0.284496736f);
+  s = __builtin_fmaf(s, t, 0.254829592f);
+  const float tail = 0.5f * s * t * e;   // P(-|g|)
+  p = g < 0.0f ? tail : 1.0f - tail;
+  d = e * 0.3989422804014327f;
+}
+
+// p with act(g) = g p: the sigmoid, the normal distribution's P, or the sigmoid that its tanh form is,
 // (1 + tanh z) / 2 = sigmoid(2 z); and act'(g) = p + g dp/dg
 template <int ACT>
-__device__ __forceinline__ float act_gate(float g) {
-  if constexpr (ACT == ACT_SILU) return sigmoid_f32(g);
-  else if constexpr (ACT == ACT_GELU) return 0.5f * (1.0f + erff(g * 0.70710678118654752f));
-  else return sigmoid_f32(1.5957691216057308f * (g + 0.044715f * g * g * g));
+__device__ __forceinline__ void act_both(float g, float& p, float& slope) {
+  if constexpr (ACT == ACT_SILU) {
+    p = sigmoid_f32(g);
+    slope = p * (1.0f + g * (1.0f - p));
+  } else if constexpr (ACT == ACT_GELU) {
+    float d;
+    normal_f32(g, p, d);
+    slope = p + g * d;
+  } else {
+    p = sigmoid_f32(1.5957691216057308f * (g + 0.044715f * g * g * g));
+    slope = p + g * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+  }
 }
 template <int ACT>
-__device__ __forceinline__ float act_slope(float g, float p) {
-  if constexpr (ACT == ACT_SILU) return p * (1.0f + g * (1.0f - p));
-  else if constexpr (ACT == ACT_GELU) return p + g * __expf(-0.5f * g * g) * 0.3989422804014327f;
-  else return p + g * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+__device__ __forceinline__ float act_gate(float g) {
+  float p, slope;
+  act_both<ACT>(g, p, slope);
+  return p;
 }
 
 }  // namespace fp4k

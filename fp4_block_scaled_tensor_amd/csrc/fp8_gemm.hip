@@ -89,7 +89,8 @@ struct F8Params {
   int64_t kp;                // bytes of an operand's row
   int kc;                    // blocks of K
   int es;                    // bytes of a scale
-  int64_t ws_row, ws_k;      // w's scales: elements between (bands of) rows, and between blocks
+  int64_t xs_row, xs_k;      // x's scales: elements between rows, and between blocks
+  int64_t ws_row, ws_k;      // w's: between (bands of) rows, and between blocks
   int ws_band;               // log2 of the rows that share a row of scales
   int64_t w_stride, ws_stride;   // bytes of one expert's codes and scales
   int n_experts;
@@ -321,9 +322,9 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
     const bool of_x = at < F::XS;
     const int r = (of_x ? at : at - F::XS) * 64 + lane;
     if (of_x) {
-      soff[j] = (uint32_t)(min((int64_t)r, m1 - 1 - m0) * p.kc * p.es);
-      ssrc[j] = uniform_ptr(p.xs + (m0 * p.kc + kc0) * p.es);
-      sstep[j] = p.es;
+      soff[j] = (uint32_t)(min((int64_t)r, m1 - 1 - m0) * p.xs_row * p.es);
+      ssrc[j] = uniform_ptr(p.xs + (m0 * p.xs_row + kc0 * p.xs_k) * p.es);
+      sstep[j] = p.xs_k * p.es;
     } else {
       const int64_t row = c0 + column(r) + (GATED && (r & (CW / 2)) ? p.F : 0);
       soff[j] = (uint32_t)((row >> p.ws_band) * p.ws_row * p.es);
@@ -552,6 +553,25 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
   }
 }
 
+// ---------------------------------------------------------------- turning scales
+// 1D scales [rows x kc] as [kc x rows]: a copy of 64 rows' scales of one block then touches a line or four
+// instead of 64. 64 x 64 at a time through the LDS.
+template <typename S>
+__global__ __launch_bounds__(256) void k_f8_turn_scales(const S* __restrict__ s, int64_t rows, int kc, S* __restrict__ out) {
+  __shared__ S tile[64][64 + 4 / sizeof(S)];
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  const int nr = (int)min(rows - r0, (int64_t)64), c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  for (int k0 = 0; k0 < kc; k0 += 64) {
+    const int nk = min(kc - k0, 64);
+    for (int r = q; r < nr; r += 4)
+      if (c < nk) tile[r][c] = s[(r0 + r) * kc + k0 + c];
+    __syncthreads();
+    for (int k = q; k < nk; k += 4)
+      if (c < nr) out[(k0 + k) * rows + r0 + c] = tile[c][k];
+    __syncthreads();
+  }
+}
+
 // ---------------------------------------------------------------- joining a split K
 // The slices' sums in slice order, rounded once to y's type.
 template <int V>
@@ -676,10 +696,25 @@ bool f8_gemm_fits(const F8GemmArgs& a) {
   return tile_grid(t) * (t.bm >= 128 ? 512 : 256) <= MAX_THREADS;
 }
 
+// The scales that are turned for a plan, at the start of the workspace: x's, and a single weight's 1D ones.
+// From 192 blocks to a compute unit on, as turning them is a launch of its own. Measured, us without / with:
+// 8192 x 4096 -> 14336 (224 blocks) 404 / 396, 8192 x 8192 -> 8192 (256) 443 / 420; but 4096 x 4096 -> 4096 (32)
+// 53 / 59, 1000 x 14336 -> 4096 (112) 73 / 78, 6144 x 8191 -> 4096 (128) 226 / 227.
+struct Turned {
+  size_t x, w;   // bytes, or 0
+};
+Turned turned(const F8GemmArgs& a, const TilePlan& t) {
+  const int64_t kc = div_up(a.x.k, F8_BLOCK);
+  if (t.bm < 256 || div_up(t.mt * t.nt, device_cu_count()) * kc < 192) return {0, 0};
+  auto bytes = [&](const F8Operand& o) { return (size_t)div_up(o.rows * div_up(o.k, F8_BLOCK) * (o.e8 ? 1 : 4), 256) * 256; };
+  return {bytes(a.x), a.w.layout == 0 && !a.offsets_given ? bytes(a.w) : 0};
+}
+
 size_t f8_gemm_ws(const F8GemmArgs& a) {
   if (a.x.rows == 0 || a.w.rows == 0) return 0;
-  const int slices = plan_tiles(a).slices;
-  return slices > 1 ? (size_t)slices * a.x.rows * a.w.rows * 4 : 0;
+  const TilePlan t = plan_tiles(a);
+  const Turned turn = turned(a, t);
+  return turn.x + turn.w + (t.slices > 1 ? (size_t)t.slices * a.x.rows * a.w.rows * 4 : 0);
 }
 
 hipError_t run_f8_gemm(const F8GemmArgs& a) {
@@ -696,6 +731,8 @@ hipError_t run_f8_gemm(const F8GemmArgs& a) {
   p.kp = kc * F8_BLOCK;
   p.kc = (int)kc;
   p.es = a.x.e8 ? 1 : 4;
+  p.xs_row = kc;
+  p.xs_k = 1;
   p.ws_row = a.w.layout == 2 ? 1 : kc;
   p.ws_k = a.w.layout == 2 ? bands : 1;
   p.ws_band = a.w.layout == 0 ? 0 : 7;
@@ -719,7 +756,18 @@ hipError_t run_f8_gemm(const F8GemmArgs& a) {
   p.mtiles = (uint32_t)t.mt;
   p.ntiles = (uint32_t)t.nt;
   p.slices = t.slices;
-  if (t.slices > 1) p.part = (float*)a.ws;
+  const Turned turn = turned(a, t);
+  auto turn_scales = [&](const F8Operand& o, void* out, const char*& s, int64_t& s_row, int64_t& s_k) {
+    const uint32_t grid = (uint32_t)div_up(o.rows, 64);
+    if (o.e8) k_f8_turn_scales<uint8_t><<<grid, 256, 0, a.stream>>>((const uint8_t*)o.s, o.rows, p.kc, (uint8_t*)out);
+    else k_f8_turn_scales<uint32_t><<<grid, 256, 0, a.stream>>>((const uint32_t*)o.s, o.rows, p.kc, (uint32_t*)out);
+    s = (const char*)out;
+    s_row = 1;
+    s_k = o.rows;
+  };
+  if (turn.x) turn_scales(a.x, a.ws, p.xs, p.xs_row, p.xs_k);
+  if (turn.w) turn_scales(a.w, (char*)a.ws + turn.x, p.ws, p.ws_row, p.ws_k);
+  if (t.slices > 1) p.part = (float*)((char*)a.ws + turn.x + turn.w);
   if (a.gated) launch<true>(a, p, t);
   else launch<false>(a, p, t);
   if (p.part) {

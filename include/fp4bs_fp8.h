@@ -56,7 +56,8 @@ typedef struct {
  * S = a' / 448 with a' = max(a, 2^-100); S = 1 for a block of zeros. The codes are
  * E4M3(x * 2^-e) or E4M3(x * (448 / a')), float32 arithmetic, nearest-even. A block that holds an
  * infinity or NaN gets NaN codes throughout and S = 1.
- * rows and cols below 2^31, fewer than 2^24 tiles of 128 x 128. Pointers a view does not write may be NULL.
+ * rows below 2^31, ld at most 2^22, fewer than 2^24 tiles of 128 x 128. Rows need only be aligned to their
+ * elements; base addresses and strides that are multiples of 16 bytes take a faster form. Pointers a view does not write may be NULL.
  */
 fp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t view,
                         int32_t scale, uint8_t* q, void* s, uint8_t* qt, void* st, void* stream);
@@ -113,7 +114,7 @@ fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_expe
  *   dh   [rows x f], gu and dgu [rows x 2 f], all of dtype (bf16 or float32), row strides lddh, ldgu, lddgu
  * fp8_gated_grad - the same as operands of the next products: q, s the row view [rows x 2 f] with 1D
  * scales (dx = dgu . W), qt, st the transposed one [2 f x rows] (dW = dgu^T . x). Either pair may be
- * NULL. f must be a multiple of 128 (pad gate and up each with zero rows).
+ * NULL. f must be a multiple of 128 (pad gate and up each with zero rows), lddh and ldgu at most 2^22.
  */
 fp4_status gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f, int64_t lddh, const void* gu,
                       int64_t ldgu, int32_t act, void* dgu, int64_t lddgu, void* stream);

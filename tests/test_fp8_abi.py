@@ -41,6 +41,7 @@ def test_quantize_rejects_bad_arguments(lib):
     assert q(rows=1 << 31) == _lib.FP4_EUNSUPPORTED
     assert q(rows=1 << 20, cols=1 << 18, ld=1 << 18) == _lib.FP4_EUNSUPPORTED   # 2^24 tiles
     assert q(ld=199) == _lib.FP4_EINVAL
+    assert q(ld=(1 << 22) + 1) == _lib.FP4_EUNSUPPORTED
     assert q(x=None) == _lib.FP4_EINVAL
     assert q(x=ctypes.c_void_p(4097)) == _lib.FP4_EALIGN
     assert q(x=ODD, dt=1) == _lib.FP4_EALIGN
