@@ -960,12 +960,14 @@ fp4_status fp8_dequantize(const fp8_operand* o, void* y, int32_t y_dtype, int64_
 fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
                               size_t* ws_bytes) {
   const char* what = "fp8_gemm_workspace";
-  if ((gated != 0 && gated != 1) || (f32 != 0 && f32 != 1)) return fail(FP4_EINVAL, "%s: gated and f32 must be 0 or 1", what);
+  if (gated < 0 || gated > 2) return fail(FP4_EINVAL, "%s: gated must be 0, 1 or 2", what);
+  if (f32 != 0 && f32 != 1) return fail(FP4_EINVAL, "%s: f32 must be 0 or 1", what);
   if (!w) return fail(FP4_EINVAL, "%s: NULL weight", what);
   if (!ws_bytes) return fail(FP4_EINVAL, "NULL size output");
   const fp8_operand x{nullptr, nullptr, w->scale, FP4_SCALES_1D, rows, w->k};
   fp4k::F8GemmArgs a{};
   a.f32 = f32 != 0;
+  a.codes = gated == 2;
   fp4_status st = check_f8_product(&x, w, n_experts, gated != 0, false, what, a);
   if (st != FP4_OK) return st;
   *ws_bytes = fp4k::f8_gemm_ws(a);
@@ -1004,6 +1006,7 @@ fp4_status fp8_gated(const fp8_operand* x, const fp8_operand* w, int32_t n_exper
   a.gated = true;
   a.act = act;
   a.ys = hs;
+  a.codes = h_kind == FP8_OUT_E4M3;
   a.f32 = h_kind == FP4_IN_FP32 || (gu && gu_dtype == FP4_IN_FP32);
   if ((st = check_f8_product(x, w, n_experts, true, true, what, a)) != FP4_OK) return st;
   const bool some = x->rows > 0 && w->rows > 0;

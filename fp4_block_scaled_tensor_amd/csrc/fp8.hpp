@@ -60,6 +60,7 @@ struct F8GemmArgs {
   const int32_t* offsets;
   bool gated;
   bool f32;          // an output is float32 (the sums are those of the bf16 matrix core)
+  bool codes;        // gated: h as E4M3 codes
   int act;
   void* y;           // y, or h of a gated product
   int y_kind;        // 0 bf16, 1 float32, 2 E4M3 with scales ys

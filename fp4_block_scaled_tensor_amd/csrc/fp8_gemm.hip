@@ -387,7 +387,9 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
     wat[0] = F::WROWS + (wn * CW + fr) * ROWB + p0, wat[1] = wat[0] - p0 + p1;
     asm("" : "+v"(xat[0]), "+v"(xat[1]), "+v"(wat[0]), "+v"(wat[1]), "+v"(xsat), "+v"(wsat));
     // the weight rows' fragments and scales of this block and, from its last products on, of the next
-    Frag wf[2][TN][WC], xf[2][WC];
+    // (WIDE: the next block's as codes, widened when it begins: two widened sets spill)
+    Frag wf[WIDE ? 1 : 2][TN][WC], xf[2][WC];
+    v8i codes[WIDE ? TN : 1];
     uint32_t sx[2], swc[2][TN];   // SC_E8: swc
     v4f swf[2][TN];               // else (BAND: of the wave's first row, or of both halves')
     auto take = [&](Frag* to, int at0, int at1) {
@@ -400,7 +402,9 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
       }
     };
     auto read_w = [&](int b, int i) {   // buffer b's, which are wf[b] and its scales
-      take(wf[b][i], wat[0] + b * F::WBUF + i * 16 * ROWB, wat[1] + b * F::WBUF + i * 16 * ROWB);
+      const int at = b * F::WBUF + i * 16 * ROWB;
+      if constexpr (WIDE) codes[i] = read_row(lds, wat[0] + at, wat[1] + at);
+      else take(wf[b][i], wat[0] + at, wat[1] + at);
       const char* s = lds + wsat + b * F::SBUF + i * 64;
       if constexpr (SC == SC_E8) {
         swc[b][i] = *reinterpret_cast<const uint32_t*>(s);
@@ -433,7 +437,13 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
     v4f held[2] = {};
     v4f hscale[2] = {};
     auto block = [&](auto parity, int copies) {
-      constexpr int W = decltype(parity)::value;   // its buffer
+      constexpr int W = decltype(parity)::value, WF = WIDE ? 0 : W;   // its buffer
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int q = 0; q < WC; ++q) wf[0][i][q] = widen8(codes[i][2 * q], codes[i][2 * q + 1]);
+      }
 #pragma unroll
       for (int n = 0; n < TM * TN; ++n) {
         const int j = n / TN, i = n % TN, slot = n - (TM * TN - SLOTS);
@@ -445,14 +455,14 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
           __syncthreads();
         }
         if constexpr (SC == SC_E8) {
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[W][i][0], xf[j & 1][0], acc[i][j], 0, 0, 0,
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[WF][i][0], xf[j & 1][0], acc[i][j], 0, 0, 0,
                                                                        (int)swc[W][i], 0, (int)sx[j & 1]);
         } else {
           v4f t = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int q = 0; q < WC; ++q) {
-            if constexpr (WIDE) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[W][i][q], xf[j & 1][q], t, 0, 0, 0);
-            else t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[W][i][q], xf[j & 1][q], t, 0, 0, 0, 0x7F, 0, 0x7F);
+            if constexpr (WIDE) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[WF][i][q], xf[j & 1][q], t, 0, 0, 0);
+            else t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[WF][i][q], xf[j & 1][q], t, 0, 0, 0, 0x7F, 0, 0x7F);
           }
           held[n & 1] = t;
           const float sxf = __uint_as_float(sx[j & 1]);
@@ -553,6 +563,140 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
   }
 }
 
+// ---------------------------------------------------------------- rows form
+// For few rows of x the weight's bytes are the bound, and a product with one launch ends before one whose split K
+// is joined by another. A workgroup owns 16 weight rows (gated: 16 features, so 32 rows) of one expert and takes
+// its rows of x 16 at a time. Its eight waves take the blocks of K in turn, four of a wave in flight at a time,
+// straight into the registers of the products (16 rows x 64 bytes to a load), and join their sums through the
+// LDS. Rows of x past the group's repeat its last one; they are not stored.
+constexpr int ROWS_NW = 8, ROWS_AHEAD = 4;
+
+template <int SC, bool GATED, int ACT>
+__global__ __launch_bounds__(ROWS_NW * 64) void k_f8_rows(F8Params p) {
+  constexpr int TN = GATED ? 2 : 1;
+  constexpr bool WIDE = SC == WIDE_E8 || SC == WIDE_F32, E8 = SC == SC_E8 || SC == WIDE_E8;
+  __shared__ v4f sums[ROWS_NW][TN][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), fr = lane & 15, kg = lane >> 4;
+  const int e = blockIdx.y;
+  int64_t lo, hi;
+  group_rows(p, e, lo, hi);
+  if (lo >= hi) return;
+  const int64_t c0 = (int64_t)blockIdx.x * 16, width = GATED ? p.F : p.N;
+  if (p.offsets && e == p.n_experts) {   // the rows of dropped slots
+    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t i = threadIdx.x; i < (hi - lo) * 4; i += ROWS_NW * 64) {
+      const int64_t m = lo + i / 4, c = c0 + i % 4 * 4;
+      const int have = (int)min(width - c, (int64_t)4);
+      if (p.part) {
+        store4((char*)p.part, true, false, m * p.N + c, have, z);
+        if (GATED) store4((char*)p.part, true, false, m * p.N + p.F + c, have, z);
+      } else {
+        if (GATED && p.gu) {
+          store4(p.gu, p.gu_f32, false, m * p.ldgu + c, have, z);
+          store4(p.gu, p.gu_f32, false, m * p.ldgu + p.F + c, have, z);
+        }
+        store4(p.y, p.out == OUT_F32, false, m * p.ldy + c, have, z);
+      }
+    }
+    return;
+  }
+  const char *wrow[TN], *wsc[TN];
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    const int64_t n = min(c0 + fr, width - 1) + i * p.F;
+    wrow[i] = p.w + (int64_t)e * p.w_stride + n * p.kp + kg * 16;
+    wsc[i] = p.ws + (int64_t)e * p.ws_stride + (n >> p.ws_band) * p.ws_row * p.es;
+  }
+  auto scale_at = [&](const char* s) {
+    if constexpr (E8) return (uint32_t)*reinterpret_cast<const uint8_t*>(s);
+    else return *reinterpret_cast<const uint32_t*>(s);
+  };
+  for (int64_t m0 = lo; m0 < hi; m0 += 16) {
+    const int64_t m = min(m0 + fr, hi - 1);
+    const char* xrow = p.x + m * p.kp + kg * 16;
+    const char* xsc = p.xs + m * p.xs_row * p.es;
+    v4f acc[TN] = {};
+    for (int k0 = wave; k0 < p.kc; k0 += ROWS_NW * ROWS_AHEAD) {
+      v4i w[ROWS_AHEAD][TN][2], x[ROWS_AHEAD][2];
+      uint32_t sw[ROWS_AHEAD][TN], sx[ROWS_AHEAD];
+#pragma unroll
+      for (int a = 0; a < ROWS_AHEAD; ++a) {
+        const int64_t k = min(k0 + a * ROWS_NW, p.kc - 1);   // (past the last block: times zeros)
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          w[a][i][0] = *reinterpret_cast<const v4i*>(wrow[i] + k * ROWB);
+          w[a][i][1] = *reinterpret_cast<const v4i*>(wrow[i] + k * ROWB + 64);
+          sw[a][i] = scale_at(wsc[i] + k * p.ws_k * p.es);
+        }
+        x[a][0] = *reinterpret_cast<const v4i*>(xrow + k * ROWB);
+        x[a][1] = *reinterpret_cast<const v4i*>(xrow + k * ROWB + 64);
+        sx[a] = scale_at(xsc + k * p.xs_k * p.es);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // all loads, then the products
+#pragma unroll
+      for (int a = 0; a < ROWS_AHEAD; ++a) {
+        const int there = k0 + a * ROWS_NW < p.kc ? -1 : 0;
+        const v8i xf = __builtin_shufflevector(x[a][0], x[a][1], 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          v8i wf = __builtin_shufflevector(w[a][i][0], w[a][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          if (a > 0) wf &= there;
+          if constexpr (SC == SC_E8) {
+            acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, acc[i], 0, 0, 0, (int)sw[a][i], 0, (int)sx[a]);
+          } else {
+            v4f t = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (WIDE) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(wf[2 * q], wf[2 * q + 1]), widen8(xf[2 * q], xf[2 * q + 1]), t, 0, 0, 0);
+            } else {
+              t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, t, 0, 0, 0, 0x7F, 0, 0x7F);
+            }
+            const float xv = E8 ? e8m0_value(sx[a]) : __uint_as_float(sx[a]), wv = E8 ? e8m0_value(sw[a][i]) : __uint_as_float(sw[a][i]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(t[r], xv * __shfl(wv, kg * 4 + r, 64), acc[i][r]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TN; ++i) sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    // lane l: x row l % 16, weight rows 4 (l / 16) + r
+    if (wave == 0) {
+      v4f v[TN];
+#pragma unroll
+      for (int i = 0; i < TN; ++i) {
+        v[i] = sums[0][i][lane];
+#pragma unroll
+        for (int s = 1; s < ROWS_NW; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[i][r] += sums[s][i][lane][r];
+      }
+      const int64_t row = m0 + fr, c = c0 + kg * 4;
+      const int have = (int)min(width - c, (int64_t)4);
+      if (row < hi && have > 0) {
+        if (p.part) {
+#pragma unroll
+          for (int i = 0; i < TN; ++i) store4((char*)p.part, true, p.N % 8 == 0, row * p.N + i * p.F + c, have, v[i]);
+        } else if constexpr (!GATED) {
+          store4(p.y, p.out == OUT_F32, p.y_vec, row * p.ldy + c, have, v[0]);
+        } else {
+          if (p.gu) {
+            store4(p.gu, p.gu_f32, p.gu_vec, row * p.ldgu + c, have, v[0]);
+            store4(p.gu, p.gu_f32, p.gu_vec, row * p.ldgu + p.F + c, have, v[TN - 1]);
+          }
+          v4f h;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) h[r] = v[0][r] * act_gate<ACT>(v[0][r]) * v[TN - 1][r];
+          store4(p.y, p.out == OUT_F32, p.y_vec, row * p.ldy + c, have, h);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // ---------------------------------------------------------------- turning scales
 // 1D scales [rows x kc] as [kc x rows]: a copy of 64 rows' scales of one block then touches a line or four
 // instead of 64. 64 x 64 at a time through the LDS.
@@ -629,27 +773,53 @@ __global__ __launch_bounds__(256) void k_f8_join_gated(F8Params p) {
 constexpr int64_t MAX_THREADS = (int64_t(1) << 32) - 1;
 
 struct TilePlan {
-  int bm;          // rows of a tile
+  int bm;          // rows of a tile; 0: the rows form
   int64_t mt, nt;  // tiles, at most
-  int slices;      // parts of K
+  int slices;      // parts of K, each with sums of its own in the workspace (rows form: 1, in the workspace for codes)
 };
 
+// Measured, us in the tile form / the rows form, bf16 out: 4096 -> 6144 E8M0, 1 row 11.5 / 8.0, 8 rows 12.2 / 9.8,
+// 16 rows 12.7 / 11.8; 14336 -> 4096, 1 row 21.1 / 13.3, 16 rows 21.6 / 19.0; 4096 -> 28672 float32 scales, 1 row
+// 27.5 / 22.5, 4 rows 27.8 / 25.9, 8 rows 28.3 / 30.2, 16 rows 29.4 / 35.7; gated 4096 -> 2 x 14336, 1 row 23.1 /
+// 25.7. Eight experts 4096 -> 14336, on average 2 rows 84 / 64, 16 rows 103 / 162; 64 of 1024 -> 2048, 4 rows 21 / 84.
+bool use_rows(const F8GemmArgs& a) {
+  const int64_t groups = a.n_experts, width = a.gated ? a.w.rows / 2 : a.w.rows;
+  const int64_t most = a.offsets_given ? 2 : a.w.rows > 16384 ? (a.gated ? 0 : 4) : 16;
+  return a.x.rows <= most * groups && div_up(width, 16) * ROWS_NW * 64 <= MAX_THREADS / (groups + 1);
+}
+
+// The tile height and number of slices whose time is least by a model of what the sweeps showed, us: a round of
+// tiles takes its blocks at BLOCK each and ROUND for its ends, but not less than the weight takes from memory;
+// slices are written and read again. (2047 x 14336 -> 4096 E8M0: 256 rows in one slice 177, in two 124, 128 rows
+// in one 151, 64 rows 220; 512 rows: 256 rows in eight slices 49, 128 in four 42, 64 in two 54; 64 x 4096 -> 28672
+// float32 scales: 64 rows in two 34, 32 in two 38, 128 in two 38.)
 TilePlan plan_tiles(const F8GemmArgs& a) {
   const int64_t cus = device_cu_count(), groups = a.offsets_given ? a.n_experts : 0, kc = div_up(a.x.k, F8_BLOCK);
+  if (use_rows(a)) return {0, 0, 0, 1};
   TilePlan best{};
   double least = 0;
+  const double weight = (double)a.w.rows * kc * F8_BLOCK * a.n_experts / 4.5e6;
   for (int bm : {256, 128, 64, 32}) {
     if (bm == 256 && a.f32) continue;   // the widened codes' registers
+    const int i = bm == 256 ? 0 : bm == 128 ? 1 : bm == 64 ? 2 : 3;
+    constexpr double BLOCK[3][4] = {{1.6, 0.9, 0.75, 0.6}, {1.6, 1.15, 1.1, 1.1}, {0.0, 1.9, 1.3, 1.1}}, ROUND[4] = {7, 5, 4, 4};
+    const int far = a.f32 ? 2 : weight > 7;   // a weight that the L2s do not hold
     TilePlan t;
     t.bm = bm;
     t.nt = a.gated ? div_up(a.w.rows / 2, BN / 2) : div_up(a.w.rows, BN);
     t.mt = div_up(a.x.rows, bm) + groups;
     const int64_t tiles = (div_up(a.x.rows, bm) + groups / 2) * t.nt;   // an expert's last tile is half full
-    t.slices = (int)std::max<int64_t>(1, std::min<int64_t>((bm <= 64 ? 2 : 1) * cus / tiles, kc / 4));
-    const double cost = (double)div_up(tiles * t.slices, cus) * (bm + 32) / t.slices;
-    if (best.bm == 0 || cost < least) {
-      best = t;
-      least = cost;
+    for (int s = 1; s <= std::max<int64_t>(1, std::min<int64_t>(kc / 4, 2 * cus / tiles)); ++s) {
+      t.slices = s;
+      // two workgroups of the lowest tiles share a compute unit, and take a third longer each
+      const bool two = bm == 32 && tiles * s > cus;
+      const double rounds = (double)div_up(tiles * s, two ? 2 * cus : cus), block = BLOCK[far][i] * (two ? 1.35 : far && t.mt == 1 && 4 * tiles * s < 3 * cus ? 1.2 : 1);
+      const double join = s > 1 ? 3 + 8e-7 * s * a.x.rows * a.w.rows : 0;
+      const double cost = std::max(rounds * div_up(kc, s) * block, weight) + rounds * ROUND[i] + join;
+      if (best.bm == 0 || cost < least) {
+        best = t;
+        least = cost;
+      }
     }
   }
   return best;
@@ -677,8 +847,22 @@ void launch_form(const F8GemmArgs& a, const F8Params& p, const TilePlan& t) {
   else launch_tile<TileForm<2, 1, SC, GATED>>(a, p, t);
 }
 
+template <int SC, bool GATED>
+void launch_rows(const F8GemmArgs& a, const F8Params& p) {
+  const dim3 grid((uint32_t)div_up(GATED ? p.F : p.N, 16), a.offsets ? a.n_experts + 1 : 1);
+  if constexpr (!GATED) k_f8_rows<SC, false, 0><<<grid, ROWS_NW * 64, 0, a.stream>>>(p);
+  else if (a.act == ACT_SILU) k_f8_rows<SC, true, ACT_SILU><<<grid, ROWS_NW * 64, 0, a.stream>>>(p);
+  else if (a.act == ACT_GELU) k_f8_rows<SC, true, ACT_GELU><<<grid, ROWS_NW * 64, 0, a.stream>>>(p);
+  else k_f8_rows<SC, true, ACT_GELU_TANH><<<grid, ROWS_NW * 64, 0, a.stream>>>(p);
+}
+
 template <bool GATED>
 void launch(const F8GemmArgs& a, const F8Params& p, const TilePlan& t) {
+  if (t.bm == 0) {
+    if (a.f32) a.x.e8 ? launch_rows<WIDE_E8, GATED>(a, p) : launch_rows<WIDE_F32, GATED>(a, p);
+    else a.x.e8 ? launch_rows<SC_E8, GATED>(a, p) : launch_rows<SC_F32_ROWS, GATED>(a, p);
+    return;
+  }
   if (a.f32) {
     if (a.x.e8) launch_form<WIDE_E8, GATED>(a, p, t);
     else launch_form<WIDE_F32, GATED>(a, p, t);
@@ -693,7 +877,7 @@ void launch(const F8GemmArgs& a, const F8Params& p, const TilePlan& t) {
 bool f8_gemm_fits(const F8GemmArgs& a) {
   if (a.x.rows == 0 || a.w.rows == 0) return true;
   const TilePlan t = plan_tiles(a);
-  return tile_grid(t) * (t.bm >= 128 ? 512 : 256) <= MAX_THREADS;
+  return t.bm == 0 || tile_grid(t) * (t.bm >= 128 ? 512 : 256) <= MAX_THREADS;
 }
 
 // The scales that are turned for a plan, at the start of the workspace: x's, and a single weight's 1D ones.
@@ -710,11 +894,15 @@ Turned turned(const F8GemmArgs& a, const TilePlan& t) {
   return {bytes(a.x), a.w.layout == 0 && !a.offsets_given ? bytes(a.w) : 0};
 }
 
+// Whether the sums go through the workspace: those of slices, and of the rows form, whose workgroups hold no whole
+// block of h, when h is wanted as codes.
+bool in_parts(const F8GemmArgs& a, const TilePlan& t) { return t.slices > 1 || (t.bm == 0 && a.codes); }
+
 size_t f8_gemm_ws(const F8GemmArgs& a) {
   if (a.x.rows == 0 || a.w.rows == 0) return 0;
   const TilePlan t = plan_tiles(a);
   const Turned turn = turned(a, t);
-  return turn.x + turn.w + (t.slices > 1 ? (size_t)t.slices * a.x.rows * a.w.rows * 4 : 0);
+  return turn.x + turn.w + (in_parts(a, t) ? (size_t)t.slices * a.x.rows * a.w.rows * 4 : 0);
 }
 
 hipError_t run_f8_gemm(const F8GemmArgs& a) {
@@ -767,7 +955,7 @@ hipError_t run_f8_gemm(const F8GemmArgs& a) {
   };
   if (turn.x) turn_scales(a.x, a.ws, p.xs, p.xs_row, p.xs_k);
   if (turn.w) turn_scales(a.w, (char*)a.ws + turn.x, p.ws, p.ws_row, p.ws_k);
-  if (t.slices > 1) p.part = (float*)((char*)a.ws + turn.x + turn.w);
+  if (in_parts(a, t)) p.part = (float*)((char*)a.ws + turn.x + turn.w);
   if (a.gated) launch<true>(a, p, t);
   else launch<false>(a, p, t);
   if (p.part) {

@@ -265,7 +265,7 @@ def fp8_gated(x: F8Tensor, w: F8Tensor | F8Experts, act: str = "silu", out_dtype
     if w.rows % 2:
         raise ValueError(f"w must stack gate and up projection, got {w.rows} rows")
     f = w.rows // 2
-    ws, nb = _work(a, b, n, 1, torch.float32 in (out_dtype, save), x.q)
+    ws, nb = _work(a, b, n, 2 if out_dtype is torch.float8_e4m3fn else 1, torch.float32 in (out_dtype, save), x.q)
     gu, gdt, ldgu = None, 0, 0
     if save is not None:
         gu, gdt, ldgu = _rows_out("gu", None, x.rows, w.rows, save, x.q)

@@ -104,8 +104,8 @@ fp4_status fp8_expert_gemm(const fp8_operand* x, const fp8_operand* w, int32_t n
 fp4_status fp8_gated(const fp8_operand* x, const fp8_operand* w, int32_t n_experts, const int32_t* offsets,
                      int32_t act, void* h, int32_t h_kind, int64_t ldh, void* hs, void* gu, int32_t gu_dtype,
                      int64_t ldgu, void* ws, size_t ws_bytes, void* stream);
-/* Bytes of ws for the three calls (n_experts 0: one weight; gated 0 or 1; f32 1 where y, h or gu is
- * float32), from rows of x and w's sizes: w's pointers are not looked at. */
+/* Bytes of ws for the three calls (n_experts 0: one weight; gated 0, 1, or 2 for h as codes; f32 1 where y, h
+ * or gu is float32), from rows of x and w's sizes: w's pointers are not looked at. */
 fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
                               size_t* ws_bytes);
 

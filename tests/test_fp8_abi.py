@@ -85,7 +85,7 @@ def test_gemm_rejects_bad_arguments(lib):
     assert g(a=op(rows=40, k=8192), b=w(), ld=4096, ws=ctypes.c_void_p(4100), nb=nb.value) == _lib.FP4_EINVAL
     assert lib.fp8_gemm_workspace(40, None, 0, 0, 0, ctypes.byref(nb)) == _lib.FP4_EINVAL
     assert lib.fp8_gemm_workspace(40, w(), 0, 0, 0, None) == _lib.FP4_EINVAL
-    assert lib.fp8_gemm_workspace(40, w(), 0, 2, 0, ctypes.byref(nb)) == _lib.FP4_EINVAL
+    assert lib.fp8_gemm_workspace(40, w(), 0, 3, 0, ctypes.byref(nb)) == _lib.FP4_EINVAL
     assert lib.fp8_gemm_workspace(40, w(), 1025, 0, 0, ctypes.byref(nb)) == _lib.FP4_EUNSUPPORTED
     assert g(a=op(rows=0)) == _lib.FP4_OK
 
