@@ -282,11 +282,13 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
   const uint32_t tiles = mtiles * p.ntiles, total = tiles * p.slices, per = (total + 7) / 8;
   const uint32_t in_die = blockIdx.x >> 3, all = (blockIdx.x & 7) * per + in_die;
   if (in_die >= per || all >= total) return;
-  const uint32_t slice = all / tiles, id = all - slice * tiles;
+  // (what stands before the first copies is short: 32-bit, and no division that a launch can do without)
+  const uint32_t slice = p.slices > 1 ? all / tiles : 0, id = all - slice * tiles;
   constexpr uint32_t GM = 4;
   const uint32_t grp = id / (GM * p.ntiles), gm = min(GM, mtiles - grp * GM), rest = id - grp * GM * p.ntiles;
-  const int mt = grp * GM + rest % gm;
-  const int64_t c0 = (int64_t)(rest / gm) * (GATED ? BN / 2 : BN);   // first column (feature)
+  const uint32_t nt = gm == GM ? rest / GM : rest / gm;
+  const int mt = grp * GM + rest - nt * gm;
+  const int64_t c0 = (int64_t)nt * (GATED ? BN / 2 : BN);   // first column (feature)
   int e = 0;
   int64_t m0 = (int64_t)mt * BM, m1 = p.rows;
   if (p.offsets) map.find(p, mt, e, m0, m1);
@@ -294,25 +296,30 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
     zero_tile<F>(p, m0, m1, c0, slice);
     return;
   }
-  const int kc0 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.kc * slice / p.slices));
-  const int kc1 = __builtin_amdgcn_readfirstlane((int)((int64_t)p.kc * (slice + 1) / p.slices));
+  int kc0 = 0, kc1 = p.kc;
+  if (p.slices > 1) {   // (kc is at most 2^15, and there are at most kc / 4 slices)
+    kc0 = __builtin_amdgcn_readfirstlane((uint32_t)p.kc * slice / (uint32_t)p.slices);
+    kc1 = __builtin_amdgcn_readfirstlane((uint32_t)p.kc * (slice + 1) / (uint32_t)p.slices);
+  }
 
   // copies: a lane's 16 bytes of an 8-row piece (rows past the tensor read its last row; not stored)
   const int64_t width = GATED ? p.F : p.N;
   const char* xsrc = uniform_ptr(p.x + m0 * p.kp + (int64_t)kc0 * ROWB);
   const char* wsrc = uniform_ptr(p.w + (int64_t)e * p.w_stride + c0 * p.kp + (int64_t)kc0 * ROWB);
   uint32_t xoff[F::XP], woff[F::WP], soff[F::SP];
+  const uint32_t kp = (uint32_t)p.kp;
+  const int last_row = (int)min(m1 - m0, (int64_t)BM) - 1, last_col = (int)min(width - c0, (int64_t)BN) - 1;
 #pragma unroll
   for (int j = 0; j < F::XP; ++j) {
     const int r = (wave * F::XP + j) * 8 + (lane >> 3);
-    xoff[j] = (uint32_t)(min((int64_t)r, m1 - 1 - m0) * p.kp) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    xoff[j] = min(r, last_row) * kp + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
   }
   // row r of the tile's weight rows: column c0 + r, or of each wave's CW the CW / 2 features' gate and up
-  auto column = [&](int r) { return min((int64_t)(GATED ? r / CW * (CW / 2) + r % (CW / 2) : r), width - 1 - c0); };
+  auto column = [&](int r) { return min(GATED ? r / CW * (CW / 2) + r % (CW / 2) : r, last_col); };
 #pragma unroll
   for (int j = 0; j < F::WP; ++j) {
     const int r = (wave * F::WP + j) * 8 + (lane >> 3);
-    woff[j] = (uint32_t)(column(r) * p.kp) + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    woff[j] = column(r) * kp + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
   }
   const char* ssrc[F::SP];
   int64_t sstep[F::SP];
@@ -322,12 +329,12 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
     const bool of_x = at < F::XS;
     const int r = (of_x ? at : at - F::XS) * 64 + lane;
     if (of_x) {
-      soff[j] = (uint32_t)(min((int64_t)r, m1 - 1 - m0) * p.xs_row * p.es);
+      soff[j] = min(r, last_row) * (uint32_t)(p.xs_row * p.es);
       ssrc[j] = uniform_ptr(p.xs + (m0 * p.xs_row + kc0 * p.xs_k) * p.es);
       sstep[j] = p.xs_k * p.es;
-    } else {
+    } else {   // (a weight's scales are below 2^32 bytes)
       const int64_t row = c0 + column(r) + (GATED && (r & (CW / 2)) ? p.F : 0);
-      soff[j] = (uint32_t)((row >> p.ws_band) * p.ws_row * p.es);
+      soff[j] = (uint32_t)(row >> p.ws_band) * (uint32_t)(p.ws_row * p.es);
       ssrc[j] = uniform_ptr(p.ws + (int64_t)e * p.ws_stride + (int64_t)kc0 * p.ws_k * p.es);
       sstep[j] = p.ws_k * p.es;
     }
