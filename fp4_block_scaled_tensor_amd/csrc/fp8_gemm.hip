@@ -144,7 +144,9 @@ template <int TM_, int WM_, int SC_, bool GATED_, int WN_ = 4>
 struct TileForm {
   static constexpr int TM = TM_, WM = WM_, SC = SC_, WN = WN_, NW = WM * WN, BM = 16 * TM * WM;
   static constexpr int TN = BN / 16 / WN, CW = TN * 16;                 // 16-row groups and weight rows of a wave
-  static constexpr bool GATED = GATED_;
+  // Streamed stores for tall tiles, us without / with: 8192 x 2048 -> 14336 232 / 210, x 4096 400 / 380, 6144 x
+  // 8191 -> 4096 227 / 183; float32 (128 rows) 390 / 385.
+  static constexpr bool GATED = GATED_, STREAM = BM >= 128;
   static constexpr int XP = BM / 8 / NW, WP = BN / 8 / NW;              // copies of 8 rows, a wave's
   static constexpr int XS = (BM + 63) / 64, SCALES = XS + BN / 64;      // copies of 64 scales, all
   static constexpr int SP = (SCALES + NW - 1) / NW;
@@ -177,11 +179,20 @@ __device__ __forceinline__ float e8m0_value(uint32_t c) {
   return __uint_as_float(c == 0 ? 1u << 22 : c == 255 ? 0x7FC00000u : c << 23);
 }
 
+// STREAM: past the L2, which keeps the operands' rows for the tiles that share them (outputs of many tiles, that
+// are next read from memory anyway).
+template <bool STREAM>
+__device__ __forceinline__ void store16(char* to, const uint4& v) {
+  typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+  if constexpr (STREAM) __builtin_nontemporal_store(u4v{v.x, v.y, v.z, v.w}, reinterpret_cast<u4v*>(to));
+  else *reinterpret_cast<uint4*>(to) = v;
+}
+
 // Columns i < NI of a wave's products (16 to a product) to rows of y, as float32 or rounded to bf16: as many of
 // its rows at a time as its share of the LDS holds, turned there so that lanes store 16 bytes of whole rows.
 // Columns from `half` of the NI on (gated: the up projection's) go `up` further on; 0: one run of columns.
 // Piece j (16 bytes) of row r stays at j ^ (r & 7) of its eight.
-template <class F, bool F32, int NI>
+template <class F, bool F32, int NI, bool STREAM>
 __device__ __forceinline__ void store_wave(char* lds, const v4f (&acc)[F::TN][F::TM], char* y, int64_t ld, bool vec,
                                            int64_t m0, int64_t m1, int64_t c0, int64_t width, int64_t up) {
   constexpr int E = F32 ? 4 : 2, COLS = NI * 16, RB = COLS * E, PIECES = RB / 16, PER = 16 / E, SW = PIECES < 8 ? PIECES - 1 : 7;
@@ -213,7 +224,7 @@ __device__ __forceinline__ void store_wave(char* lds, const v4f (&acc)[F::TN][F:
         if (m >= m1 || c0 + in >= width) continue;
         char* to = y + (m * ld + c0 + in + (c >= half ? up : 0)) * E;
         if (c0 + in + PER <= width) {
-          *reinterpret_cast<uint4*>(to) = v;
+          store16<STREAM>(to, v);
         } else {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           for (int q = 0; q < (int)(width - c0) - in; ++q) {
@@ -507,14 +518,14 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
   // through LDS rows of its own.
   const int64_t wrow0 = m0 + wm * TM * 16, f0 = c0 + wn * (GATED ? CW / 2 : CW);
   __syncthreads();
-  if (p.part) store_wave<F, true, TN>(lds, acc, reinterpret_cast<char*>(p.part + (int64_t)slice * p.rows * p.N), p.N,
+  if (p.part) store_wave<F, true, TN, false>(lds, acc, reinterpret_cast<char*>(p.part + (int64_t)slice * p.rows * p.N), p.N,
                                       p.N % 4 == 0 && p.F % 4 == 0, wrow0, m1, f0, width, p.F);
   else if constexpr (!GATED) {
-    if (p.out == OUT_F32) store_wave<F, true, TN>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
-    else store_wave<F, false, TN>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
+    if (p.out == OUT_F32) store_wave<F, true, TN, F::STREAM>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
+    else store_wave<F, false, TN, F::STREAM>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
   } else {
-    if (p.gu && p.gu_f32) store_wave<F, true, TN>(lds, acc, p.gu, p.ldgu, p.gu_vec, wrow0, m1, f0, width, p.F);
-    else if (p.gu) store_wave<F, false, TN>(lds, acc, p.gu, p.ldgu, p.gu_vec, wrow0, m1, f0, width, p.F);
+    if (p.gu && p.gu_f32) store_wave<F, true, TN, F::STREAM>(lds, acc, p.gu, p.ldgu, p.gu_vec, wrow0, m1, f0, width, p.F);
+    else if (p.gu) store_wave<F, false, TN, F::STREAM>(lds, acc, p.gu, p.ldgu, p.gu_vec, wrow0, m1, f0, width, p.F);
 #pragma unroll
     for (int j = 0; j < TM; ++j)
 #pragma unroll
@@ -524,8 +535,8 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
           const float g = acc[i][j][r];
           acc[i][j][r] = g * act_gate<ACT>(g) * acc[i + TN / 2][j][r];
         }
-    if (p.out == OUT_F32) store_wave<F, true, TN / 2>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
-    else if (p.out == OUT_BF16) store_wave<F, false, TN / 2>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
+    if (p.out == OUT_F32) store_wave<F, true, TN / 2, F::STREAM>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
+    else if (p.out == OUT_BF16) store_wave<F, false, TN / 2, F::STREAM>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
   }
   if constexpr (GATED) {
     if (p.part || p.out != OUT_F8) return;
@@ -564,8 +575,7 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
     for (int i = threadIdx.x; i < BM * 8; i += NW * 64) {
       const int row = i >> 3, piece = i & 7;
       if (m0 + row < m1)
-        *reinterpret_cast<uint4*>(p.y + (m0 + row) * p.ldy + c0 + piece * 16) =
-            *reinterpret_cast<const uint4*>(lds + row * F8_BLOCK + piece * 16);
+        store16<F::STREAM>(p.y + (m0 + row) * p.ldy + c0 + piece * 16, *reinterpret_cast<const uint4*>(lds + row * F8_BLOCK + piece * 16));
     }
   }
 }

@@ -5,7 +5,9 @@
 // input serves all of them. Thread (tr, tc) = (id / 16, id % 16) holds the P x 8 elements of rows
 // P tr .. and columns 8 tc ..: a row's block is 16 neighbouring lanes, a column's one lane in 16 of
 // every wave. Row codes go straight to memory, 128 consecutive bytes from 16 lanes; column codes turn
-// in LDS, where a thread has P consecutive bytes of each of its columns.
+// in LDS, where a thread has P consecutive bytes of each of its columns. Codes are stored past the L2 (8192 x
+// 4096 bf16, both views: 31.6 -> 28.6 us). Bound by HBM: 4.7 TB/s there, 5.5 for one view or 28672 x 4096 float32 in
+// tiles, against 5.2 of a copy.
 #include "fp8.hpp"
 #include "quant_common.hpp"
 
@@ -173,10 +175,9 @@ __device__ __forceinline__ void quantize_tile(const float (&v)[S::P][8], const T
         if (tc == 0 && r < t.rows) store_scale<E8>(o.s, (o.row0 + r) * o.sld + o.col0 / T, s.code);
       }
       if (r < t.rows) {   // (codes past the columns are those of the zeros there)
-        uint2 w;
-        w.x = f8_pack4(v[p][0] * enc, v[p][1] * enc, v[p][2] * enc, v[p][3] * enc);
-        w.y = f8_pack4(v[p][4] * enc, v[p][5] * enc, v[p][6] * enc, v[p][7] * enc);
-        *reinterpret_cast<uint2*>(o.q + (o.row0 + r) * o.kp + o.col0 + tc * 8) = w;
+        const v2u w = {f8_pack4(v[p][0] * enc, v[p][1] * enc, v[p][2] * enc, v[p][3] * enc),
+                       f8_pack4(v[p][4] * enc, v[p][5] * enc, v[p][6] * enc, v[p][7] * enc)};
+        __builtin_nontemporal_store(w, reinterpret_cast<v2u*>(o.q + (o.row0 + r) * o.kp + o.col0 + tc * 8));
       }
     }
   }
@@ -220,8 +221,8 @@ __device__ __forceinline__ void quantize_tile(const float (&v)[S::P][8], const T
     for (int i = 0; i < T * T / 16 / S::THREADS; ++i) {
       const int at = i * S::THREADS + tid, c = at >> 3, piece = at & 7;
       if (c < t.cols)   // (codes past the rows are those of the zeros there)
-        *reinterpret_cast<uint4*>(o.qt + (o.trow0 + c) * o.ktp + o.tcol0 + piece * 16) =
-            *reinterpret_cast<const uint4*>(lds.codes + c * T + ((piece ^ ((c >> 3) & 7)) << 4));
+        __builtin_nontemporal_store(*reinterpret_cast<const v4u*>(lds.codes + c * T + ((piece ^ ((c >> 3) & 7)) << 4)),
+                                    reinterpret_cast<v4u*>(o.qt + (o.trow0 + c) * o.ktp + o.tcol0 + piece * 16));
     }
   }
 }
