@@ -133,16 +133,14 @@ __device__ __forceinline__ F8Scale hs_scale(const F8Params& p, uint32_t amax) {
 }
 
 // ---------------------------------------------------------------- tile form
-// A workgroup owns BM = 16 TM WM rows of x and 256 rows of a weight (gated: 128 of the gate's and the same
-// 128 of the up projection's): WM x 4 waves of 16 TM x 64 outputs. The two operands' rows of one block of
+// A workgroup owns BM = 16 TM WM rows of x and BN = 256 rows of a weight (gated: 128 of the gate's and the same
+// 128 of the up projection's), or half as many where rows are few: WM x 4 waves of 16 TM x BN / 4 outputs. The two operands' rows of one block of
 // K, and their scales, are copied straight into LDS, two blocks deep. Row r (128 bytes) keeps its 16-byte
 // piece j at j ^ ((r >> 1) & 7), so that 16 rows reading one piece fall on all banks.
 constexpr int ROWB = F8_BLOCK;
-constexpr int BN = 256;   // weight rows of a tile
-
-template <int TM_, int WM_, int SC_, bool GATED_, int WN_ = 4>
+template <int TM_, int WM_, int BN_, int SC_, bool GATED_>
 struct TileForm {
-  static constexpr int TM = TM_, WM = WM_, SC = SC_, WN = WN_, NW = WM * WN, BM = 16 * TM * WM;
+  static constexpr int TM = TM_, WM = WM_, BN = BN_, SC = SC_, WN = 4, NW = WM * WN, BM = 16 * TM * WM;
   static constexpr int TN = BN / 16 / WN, CW = TN * 16;                 // 16-row groups and weight rows of a wave
   // Streamed stores for tall tiles, us without / with: 8192 x 2048 -> 14336 232 / 210, x 4096 400 / 380, 6144 x
   // 8191 -> 4096 227 / 183; float32 (128 rows) 390 / 385.
@@ -253,7 +251,7 @@ __device__ __forceinline__ void store_wave(char* lds, const v4f (&acc)[F::TN][F:
 template <class F>
 __device__ __forceinline__ void zero_tile(const F8Params& p, int64_t m0, int64_t m1, int64_t c0, int slice) {
   const int rows = (int)min((int64_t)F::BM, m1 - m0);
-  constexpr int W = F::GATED ? BN / 2 : BN;
+  constexpr int W = F::GATED ? F::BN / 2 : F::BN;
   const int64_t width = F::GATED ? p.F : p.N;
   const int cols = (int)min((int64_t)W, width - c0);
   const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -280,8 +278,8 @@ __device__ __forceinline__ void zero_tile(const F8Params& p, int64_t m0, int64_t
 }
 
 template <class F, int ACT>
-__global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_tile(F8Params p) {
-  constexpr int TM = F::TM, TN = F::TN, WN = F::WN, CW = F::CW, NW = F::NW, BM = F::BM, SC = F::SC;
+__global__ __launch_bounds__(F::NW * 64, 2) void k_f8_tile(F8Params p) {
+  constexpr int TM = F::TM, TN = F::TN, WN = F::WN, BN = F::BN, CW = F::CW, NW = F::NW, BM = F::BM, SC = F::SC;
   constexpr bool GATED = F::GATED;
   __shared__ __attribute__((aligned(1024))) char lds[F::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -539,7 +537,7 @@ __global__ __launch_bounds__(F::NW * 64, F::TM * F::TN > 32 ? 1 : 2) void k_f8_t
     else if (p.out == OUT_BF16) store_wave<F, false, TN / 2, F::STREAM>(lds, acc, p.y, p.ldy, p.y_vec, wrow0, m1, f0, width, 0);
   }
   if constexpr (GATED) {
-    if (p.part || p.out != OUT_F8) return;
+    if (p.part || p.out != OUT_F8 || BN != 2 * F8_BLOCK) return;
     // h as codes: the waves across hold the 128 features of a row's block
     uint32_t* red = reinterpret_cast<uint32_t*>(lds + F::CODES);   // [WN][BM]
     __syncthreads();
@@ -790,7 +788,7 @@ __global__ __launch_bounds__(256) void k_f8_join_gated(F8Params p) {
 constexpr int64_t MAX_THREADS = (int64_t(1) << 32) - 1;
 
 struct TilePlan {
-  int bm;          // rows of a tile; 0: the rows form
+  int bm, bn;      // rows and columns of a tile; bm 0: the rows form
   int64_t mt, nt;  // tiles, at most
   int slices;      // parts of K, each with sums of its own in the workspace (rows form: 1, in the workspace for codes)
 };
@@ -805,32 +803,41 @@ bool use_rows(const F8GemmArgs& a) {
   return a.x.rows <= most * groups && div_up(width, 16) * ROWS_NW * 64 <= MAX_THREADS / (groups + 1);
 }
 
-// The tile height and number of slices whose time is least by a model of what the sweeps showed, us: a round of
-// tiles takes its blocks at BLOCK each and ROUND for its ends, but not less than the weight takes from memory;
-// slices are written and read again. (2047 x 14336 -> 4096 E8M0: 256 rows in one slice 177, in two 124, 128 rows
+// The tile and number of slices whose time is least by a model of what the sweeps showed, us: a round of tiles
+// takes its blocks at BLOCK each and ROUND for its ends, but not less than the weight takes from memory; slices are
+// written and read again. (2047 x 14336 -> 4096 E8M0: 256 rows in one slice 177, in two 124, 128 rows
 // in one 151, 64 rows 220; 512 rows: 256 rows in eight slices 49, 128 in four 42, 64 in two 54; 64 x 4096 -> 28672
-// float32 scales: 64 rows in two 34, 32 in two 38, 128 in two 38.)
+// float32 scales: 64 rows in two 34, 32 in two 38, 128 in two 38. 128 columns instead of 256: 1000 x 1000 -> 1000
+// 8.0 -> 5.5, but 17 x 4096 -> 28672 from memory, 256 columns in two slices 30.7, 128 in one 34.5.)
 TilePlan plan_tiles(const F8GemmArgs& a) {
   const int64_t cus = device_cu_count(), groups = a.offsets_given ? a.n_experts : 0, kc = div_up(a.x.k, F8_BLOCK);
-  if (use_rows(a)) return {0, 0, 0, 1};
+  if (use_rows(a)) return {0, 0, 0, 0, 1};
   TilePlan best{};
   double least = 0;
   const double weight = (double)a.w.rows * kc * F8_BLOCK * a.n_experts / 4.5e6;
-  for (int bm : {256, 128, 64, 32}) {
-    if (bm == 256 && a.f32) continue;   // the widened codes' registers
-    const int i = bm == 256 ? 0 : bm == 128 ? 1 : bm == 64 ? 2 : 3;
-    constexpr double BLOCK[3][4] = {{1.6, 0.9, 0.75, 0.6}, {1.6, 1.15, 1.1, 1.1}, {0.0, 1.9, 1.3, 1.1}}, ROUND[4] = {7, 5, 4, 4};
-    const int far = a.f32 ? 2 : weight > 7;   // a weight that the L2s do not hold
+  // us a block and a round, for a weight that the L2s hold, for one that they do not, and for widened codes
+  constexpr int BM[5] = {256, 128, 64, 32, 32};
+  constexpr double BLOCK[3][5] = {{1.6, 0.9, 0.75, 0.6, 0.5}, {1.6, 1.15, 1.1, 1.1, 1.15}, {0.0, 1.9, 1.3, 1.1, 0.75}};
+  constexpr double ROUND[5] = {7, 5, 4, 4, 4};
+  const bool far = weight > 7;
+  for (int i = 0; i < 5; ++i) {
+    const int bm = BM[i];
+    if (bm == 256 && a.f32) continue;    // the widened codes' registers
+    if (i == 4 && a.codes) continue;     // a tile holds whole blocks of h
     TilePlan t;
     t.bm = bm;
-    t.nt = a.gated ? div_up(a.w.rows / 2, BN / 2) : div_up(a.w.rows, BN);
+    t.bn = i == 4 ? 128 : 256;
+    t.nt = a.gated ? div_up(a.w.rows / 2, t.bn / 2) : div_up(a.w.rows, t.bn);
     t.mt = div_up(a.x.rows, bm) + groups;
     const int64_t tiles = (div_up(a.x.rows, bm) + groups / 2) * t.nt;   // an expert's last tile is half full
     for (int s = 1; s <= std::max<int64_t>(1, std::min<int64_t>(kc / 4, 2 * cus / tiles)); ++s) {
       t.slices = s;
       // two workgroups of the lowest tiles share a compute unit, and take a third longer each
       const bool two = bm == 32 && tiles * s > cus;
-      const double rounds = (double)div_up(tiles * s, two ? 2 * cus : cus), block = BLOCK[far][i] * (two ? 1.35 : far && t.mt == 1 && 4 * tiles * s < 3 * cus ? 1.2 : 1);
+      // and one row of tiles on few of them does not draw the memory's rate
+      const bool few = (far || a.f32) && t.mt == 1 && 4 * tiles * s < 3 * cus;
+      const double rounds = (double)div_up(tiles * s, two ? 2 * cus : cus);
+      const double block = BLOCK[a.f32 ? 2 : far][i] * (two ? 1.35 : few ? 1.2 : 1);
       const double join = s > 1 ? 3 + 8e-7 * s * a.x.rows * a.w.rows : 0;
       const double cost = std::max(rounds * div_up(kc, s) * block, weight) + rounds * ROUND[i] + join;
       if (best.bm == 0 || cost < least) {
@@ -857,11 +864,12 @@ void launch_tile(const F8GemmArgs& a, const F8Params& p, const TilePlan& t) {
 template <int SC, bool GATED>
 void launch_form(const F8GemmArgs& a, const F8Params& p, const TilePlan& t) {
   if constexpr (SC < WIDE_E8) {
-    if (t.bm == 256) return launch_tile<TileForm<8, 2, SC, GATED>>(a, p, t);
+    if (t.bm == 256) return launch_tile<TileForm<8, 2, 256, SC, GATED>>(a, p, t);
   }
-  if (t.bm == 128) launch_tile<TileForm<4, 2, SC, GATED>>(a, p, t);
-  else if (t.bm == 64) launch_tile<TileForm<4, 1, SC, GATED>>(a, p, t);
-  else launch_tile<TileForm<2, 1, SC, GATED>>(a, p, t);
+  if (t.bm == 128) launch_tile<TileForm<4, 2, 256, SC, GATED>>(a, p, t);
+  else if (t.bm == 64) launch_tile<TileForm<4, 1, 256, SC, GATED>>(a, p, t);
+  else if (t.bn == 256) launch_tile<TileForm<2, 1, 256, SC, GATED>>(a, p, t);
+  else launch_tile<TileForm<2, 1, 128, SC, GATED>>(a, p, t);
 }
 
 template <int SC, bool GATED>
