@@ -143,7 +143,8 @@ __device__ __forceinline__ void act_both(float g, float& p, float& slope) {
     slope = p + g * d;
   } else {
     p = sigmoid_f32(1.5957691216057308f * (g + 0.044715f * g * g * g));
-    slope = p + g * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+    const float c = fminf(fmaxf(g, -64.0f), 64.0f);   // (p (1 - p) is 0 from there on, and g^2 may be infinite)
+    slope = p + c * p * (1.0f - p) * 1.5957691216057308f * (1.0f + 0.134145f * c * c);
   }
 }
 template <int ACT>

@@ -57,7 +57,7 @@ __device__ __forceinline__ void lds_dma_scale_masked(const void* sbase, uint32_t
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
         "s_mov_b32 exec_lo, %3\n\t"
-      "s_mov_b32 exec_hi, %3\n\t"
+        "s_mov_b32 exec_hi, %3\n\t"
         "s_nop 0\n\t"
         "global_load_lds_ubyte %0, %1\n\t"
         "s_mov_b64 exec, -1"
@@ -68,7 +68,7 @@ __device__ __forceinline__ void lds_dma_scale_masked(const void* sbase, uint32_t
     asm volatile(
         "s_mov_b32 m0, %2\n\t"
         "s_mov_b32 exec_lo, %3\n\t"
-      "s_mov_b32 exec_hi, %3\n\t"
+        "s_mov_b32 exec_hi, %3\n\t"
         "s_nop 0\n\t"
         "global_load_lds_dword %0, %1\n\t"
         "s_mov_b64 exec, -1"
@@ -134,9 +134,14 @@ __device__ __forceinline__ F8Scale hs_scale(const F8Params& p, uint32_t amax) {
 
 // ---------------------------------------------------------------- tile form
 // A workgroup owns BM = 16 TM WM rows of x and BN = 256 rows of a weight (gated: 128 of the gate's and the same
-// 128 of the up projection's), or half as many where rows are few: WM x 4 waves of 16 TM x BN / 4 outputs. The two operands' rows of one block of
-// K, and their scales, are copied straight into LDS, two blocks deep. Row r (128 bytes) keeps its 16-byte
-// piece j at j ^ ((r >> 1) & 7), so that 16 rows reading one piece fall on all banks.
+// 128 of the up projection's), or half as many where rows are few: WM x 4 waves of 16 TM x BN / 4 outputs. The
+// two operands' rows of one block of K, and their scales, are copied straight into LDS, two blocks deep. Row r
+// (128 bytes) keeps its 16-byte piece j at j ^ ((r >> 1) & 7), so that 16 rows reading one piece fall on all banks.
+//
+// Tall tiles are bound by the matrix cores, at 58% of their cycles for 256 rows: a block takes 1.43 to 1.6 us
+// against 1.02 of its products alone; without its copies it takes 1.26. 8192 x 4096 -> 14336 380 us with E8M0
+// scales (2.5 PFLOP/s), 455 with float32 ones, whose multiply-adds are the vector unit's; widened codes 1.1 PFLOP/s.
+// Low tiles are bound by the weight's bytes and a block's latency (17 x 4096 -> 28672 31 us, 3.8 TB/s).
 constexpr int ROWB = F8_BLOCK;
 template <int TM_, int WM_, int BN_, int SC_, bool GATED_>
 struct TileForm {
@@ -669,7 +674,10 @@ __global__ __launch_bounds__(ROWS_NW * 64) void k_f8_rows(F8Params p) {
             }
             const float xv = E8 ? e8m0_value(sx[a]) : __uint_as_float(sx[a]), wv = E8 ? e8m0_value(sw[a][i]) : __uint_as_float(sw[a][i]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][r] = __builtin_fmaf(t[r], xv * __shfl(wv, kg * 4 + r, 64), acc[i][r]);
+            for (int r = 0; r < 4; ++r) {
+              const float scale = xv * __shfl(wv, kg * 4 + r, 64);
+              acc[i][r] = __builtin_fmaf(t[r], a == 0 || there ? scale : 0.0f, acc[i][r]);   // (it may be infinite)
+            }
           }
         }
       }
@@ -718,16 +726,18 @@ __global__ __launch_bounds__(ROWS_NW * 64) void k_f8_rows(F8Params p) {
 template <typename S>
 __global__ __launch_bounds__(256) void k_f8_turn_scales(const S* __restrict__ s, int64_t rows, int kc, S* __restrict__ out) {
   __shared__ S tile[64][64 + 4 / sizeof(S)];
-  const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int nr = (int)min(rows - r0, (int64_t)64), c = threadIdx.x & 63, q = threadIdx.x >> 6;
-  for (int k0 = 0; k0 < kc; k0 += 64) {
-    const int nk = min(kc - k0, 64);
-    for (int r = q; r < nr; r += 4)
-      if (c < nk) tile[r][c] = s[(r0 + r) * kc + k0 + c];
-    __syncthreads();
-    for (int k = q; k < nk; k += 4)
-      if (c < nr) out[(k0 + k) * rows + r0 + c] = tile[c][k];
-    __syncthreads();
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  for (int64_t r0 = (int64_t)blockIdx.x * 64; r0 < rows; r0 += (int64_t)gridDim.x * 64) {
+    const int nr = (int)min(rows - r0, (int64_t)64);
+    for (int k0 = 0; k0 < kc; k0 += 64) {
+      const int nk = min(kc - k0, 64);
+      for (int r = q; r < nr; r += 4)
+        if (c < nk) tile[r][c] = s[(r0 + r) * kc + k0 + c];
+      __syncthreads();
+      for (int k = q; k < nk; k += 4)
+        if (c < nr) out[(k0 + k) * rows + r0 + c] = tile[c][k];
+      __syncthreads();
+    }
   }
 }
 
@@ -971,7 +981,7 @@ hipError_t run_f8_gemm(const F8GemmArgs& a) {
   p.slices = t.slices;
   const Turned turn = turned(a, t);
   auto turn_scales = [&](const F8Operand& o, void* out, const char*& s, int64_t& s_row, int64_t& s_k) {
-    const uint32_t grid = (uint32_t)div_up(o.rows, 64);
+    const uint32_t grid = (uint32_t)std::min<int64_t>(div_up(o.rows, 64), 1 << 20);
     if (o.e8) k_f8_turn_scales<uint8_t><<<grid, 256, 0, a.stream>>>((const uint8_t*)o.s, o.rows, p.kc, (uint8_t*)out);
     else k_f8_turn_scales<uint32_t><<<grid, 256, 0, a.stream>>>((const uint32_t*)o.s, o.rows, p.kc, (uint32_t*)out);
     s = (const char*)out;

@@ -57,7 +57,8 @@ typedef struct {
  * E4M3(x * 2^-e) or E4M3(x * (448 / a')), float32 arithmetic, nearest-even. A block that holds an
  * infinity or NaN gets NaN codes throughout and S = 1.
  * rows below 2^31, ld at most 2^22, fewer than 2^24 tiles of 128 x 128. Rows need only be aligned to their
- * elements; base addresses and strides that are multiples of 16 bytes take a faster form. Pointers a view does not write may be NULL.
+ * elements; base addresses and strides that are multiples of 16 bytes take a faster form. Pointers a view
+ * does not write may be NULL.
  */
 fp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t view,
                         int32_t scale, uint8_t* q, void* s, uint8_t* qt, void* st, void* stream);
@@ -94,7 +95,7 @@ fp4_status fp8_dequantize(const fp8_operand* a, void* y, int32_t y_dtype, int64_
  * act and the product are taken in float32 on the unrounded projections, whose sums are those of a
  * float32 y above where h or gu is float32, and those of a bf16 y otherwise.
  *
- * Calls whose output tiles (of at least 32 x 256, and one more row of tiles to an expert) are 2^23
+ * Calls whose output tiles (of at least 32 x 128, and one more row of tiles to an expert) are 2^23
  * or more return FP4_EUNSUPPORTED.
  */
 fp4_status fp8_gemm(const fp8_operand* a, const fp8_operand* b, void* y, int32_t y_dtype, int64_t ldy, void* ws,
@@ -111,7 +112,8 @@ fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_expe
 
 /*
  * gated_grad - dgu[m][j] = dh u act'(g), dgu[m][f + j] = dh act(g) in float32, rounded once.
- *   dh   [rows x f], gu and dgu [rows x 2 f], all of dtype (bf16 or float32), row strides lddh, ldgu, lddgu
+ *   dh   [rows x f], gu and dgu [rows x 2 f], all of dtype (bf16 or float32), row strides lddh, ldgu, lddgu;
+ *        dgu may be gu itself (same stride)
  * fp8_gated_grad - the same as operands of the next products: q, s the row view [rows x 2 f] with 1D
  * scales (dx = dgu . W), qt, st the transposed one [2 f x rows] (dW = dgu^T . x). Either pair may be
  * NULL. f must be a multiple of 128 (pad gate and up each with zero rows), lddh and ldgu at most 2^22.
