@@ -1045,8 +1045,8 @@ fp4_status fp8_gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f
   if (f % 128) return fail(FP4_EUNSUPPORTED, "%s: f must be a multiple of 128 (got %lld)", what, (long long)f);
   if (lddh > MAX_WIDTH || ldgu > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: lddh and ldgu must be at most 2^22", what);
   if (((rows + 127) / 128) * (f / 128) >= MAX_F8_TILES) return fail(FP4_EUNSUPPORTED, "%s: 2^24 tiles or more", what);
-  if (!q && !qt) return fail(FP4_EINVAL, "%s: no view to write", what);
   if (rows > 0 && f > 0) {
+    if (!q && !qt) return fail(FP4_EINVAL, "%s: no view to write", what);
     if (q && (e = check_f8_out(q, s, scale, what, "row view")) != FP4_OK) return e;
     if (qt && (e = check_f8_out(qt, st, scale, what, "transposed view")) != FP4_OK) return e;
   }
