@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 from dataclasses import dataclass
 
 import torch
@@ -93,15 +94,20 @@ def _operand(a: F8Tensor | F8Experts, name: str, device: torch.device, n_experts
 
 def _on_device_of(f):
     """f with the device of its first operand's codes made current (the library launches on the current one)."""
+    first = next(iter(inspect.signature(f).parameters))
+
     @functools.wraps(f)
-    def call(a, *args, **kwargs):
+    def call(*args, **kwargs):
+        a = args[0] if args else kwargs.get(first)
+        if a is None:   # (f names the missing operand)
+            return f(*args, **kwargs)
         if not a.q.is_cuda:
             raise ValueError("FP8 kernels take device tensors (the path has no CPU implementation)")
         device = a.q.get_device()
         if device == _current_device():
-            return f(a, *args, **kwargs)
+            return f(*args, **kwargs)
         with torch.cuda.device(device):
-            return f(a, *args, **kwargs)
+            return f(*args, **kwargs)
     return call
 
 

@@ -1,0 +1,34 @@
+"""The 8-bit operators' binding on the host: operands by keyword, and what may be an operand (no GPU needed)."""
+import pytest
+import torch
+
+import fp4_block_scaled_tensor_amd as fp4
+
+
+def host_operand(rows=4, k=128):
+    return fp4.F8Tensor(torch.zeros(rows, k, dtype=torch.uint8), torch.zeros(rows, 1), fp4.FP4_SCALES_1D, rows, k)
+
+
+def host_stack():
+    return fp4.F8Experts(torch.zeros(2, 4, 128, dtype=torch.uint8), torch.zeros(2, 4, 1), fp4.FP4_SCALES_1D, 4, 128)
+
+
+@pytest.mark.parametrize("name,arguments", [
+    ("fp8_gemm", lambda: dict(a=host_operand(), b=host_operand())),
+    ("fp8_gemm", lambda: dict(b=host_operand(), a=host_operand())),
+    ("fp8_expert_gemm", lambda: dict(x=host_operand(), w=host_stack(), plan=torch.zeros(3, dtype=torch.int32))),
+    ("fp8_gated", lambda: dict(x=host_operand(), w=host_operand())),
+    ("fp8_gated", lambda: dict(w=host_operand(), act="gelu", x=host_operand())),
+    ("fp8_dequantize", lambda: dict(a=host_operand())),
+])
+def test_operands_by_keyword(name, arguments):
+    """The call gets as far as the first operand's own check."""
+    with pytest.raises(ValueError, match="device tensors"):
+        getattr(fp4, name)(**arguments())
+
+
+def test_a_missing_operand_is_named():
+    with pytest.raises(TypeError, match="'x'"):
+        fp4.fp8_gated(w=host_operand())
+    with pytest.raises(TypeError, match="'a'"):
+        fp4.fp8_gemm()
