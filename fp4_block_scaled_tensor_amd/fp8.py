@@ -25,6 +25,7 @@ BLOCK = 128
 ACTIVATIONS = {"silu": _lib.FP8_ACT_SILU, "gelu": _lib.FP8_ACT_GELU, "gelu_tanh": _lib.FP8_ACT_GELU_TANH}
 _SCALE_DTYPES = {F8_SCALE_E8M0: torch.float8_e8m0fnu, F8_SCALE_F32: torch.float32}
 _BYTES = (torch.uint8, torch.float8_e8m0fnu)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
 @dataclass
@@ -77,9 +78,9 @@ def _operand(a: F8Tensor | F8Experts, name: str, device: torch.device, n_experts
     """The C operand of a (one expert's of a stack) after its tensors are checked against its sizes."""
     q, s, many = a.q, a.s, n_experts or 1
     rows, cols = _scale_shape(a.layout, a.rows, a.k)
-    if q.element_size() != 1 or q.numel() != many * a.rows * _blocks(a.k) * BLOCK or not q.is_contiguous() or q.device != device:
-        raise ValueError(f"{name}: codes must be a contiguous tensor of {many * a.rows * _blocks(a.k) * BLOCK} bytes on "
-                         f"{device}, got {q.dtype} {tuple(q.shape)} on {q.device}")
+    if q.dtype not in _CODES or q.numel() != many * a.rows * _blocks(a.k) * BLOCK or not q.is_contiguous() or q.device != device:
+        raise ValueError(f"{name}: codes must be a contiguous float8_e4m3fn (or uint8) tensor of "
+                         f"{many * a.rows * _blocks(a.k) * BLOCK} bytes on {device}, got {q.dtype} {tuple(q.shape)} on {q.device}")
     if s.dtype in _BYTES:
         scale = F8_SCALE_E8M0
     elif s.dtype is torch.float32:

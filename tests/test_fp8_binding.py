@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import fp4_block_scaled_tensor_amd as fp4
+from fp4_block_scaled_tensor_amd import fp8
 
 
 def host_operand(rows=4, k=128):
@@ -32,3 +33,20 @@ def test_a_missing_operand_is_named():
         fp4.fp8_gated(w=host_operand())
     with pytest.raises(TypeError, match="'a'"):
         fp4.fp8_gemm()
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz, torch.float8_e8m0fnu,
+                                   torch.int8, torch.bool])
+def test_codes_of_another_type_are_refused(dtype):
+    """One byte each, but not E4M3."""
+    dev, q = torch.device("cpu"), torch.zeros(4, 256, dtype=torch.uint8).view(dtype)
+    with pytest.raises(ValueError, match="codes must be"):
+        fp8._operand(fp4.F8Tensor(q, torch.zeros(4, 2), fp4.FP4_SCALES_1D, 4, 200), "a", dev)
+    with pytest.raises(ValueError, match="codes must be"):
+        fp8._operand(fp4.F8Experts(q[None], torch.zeros(1, 4, 2), fp4.FP4_SCALES_1D, 4, 200), "w", dev, 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float8_e4m3fn, torch.uint8])
+def test_codes_of_the_right_types(dtype):
+    q = torch.zeros(4, 256, dtype=torch.uint8).view(dtype)
+    assert fp8._operand(fp4.F8Tensor(q, torch.zeros(4, 2), fp4.FP4_SCALES_1D, 4, 200), "a", torch.device("cpu")).rows == 4
