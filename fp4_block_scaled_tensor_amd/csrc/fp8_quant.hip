@@ -269,7 +269,8 @@ template <int ACT>
 __device__ __forceinline__ void gated_grad1(float dh, float g, float u, float& dg, float& du) {
   float p, slope;
   act_both<ACT>(g, p, slope);
-  dg = dh * (u * slope);   // (a slope of 0 meets no infinite dh u)
+  // (a slope of 0 meets no infinite dh u; half of one, which is below 1, takes no u past the range)
+  dg = 2.0f * (dh * (u * (0.5f * slope)));
   du = dh * (g * p);
 }
 
