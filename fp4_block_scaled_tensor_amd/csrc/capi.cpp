@@ -415,8 +415,6 @@ fp4_status check_gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t
   return FP4_OK;
 }
 
-constexpr int64_t MAX_F8_TILES = int64_t(1) << 24;   // workgroups of 256 threads in a launch
-
 }  // namespace
 
 extern "C" {
@@ -931,7 +929,7 @@ fp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t co
   if (rows < 0 || cols < 0) return fail(FP4_EINVAL, "%s: negative size", what);
   if (rows > MAX_SLOTS || cols > MAX_SLOTS) return fail(FP4_EUNSUPPORTED, "%s: rows and cols must be below 2^31", what);
   if (ld > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: ld must be at most 2^22", what);
-  if (((rows + 127) / 128) * ((cols + 127) / 128) >= MAX_F8_TILES)
+  if (!fp4k::f8_quantize_fits(rows, cols))
     return fail(FP4_EUNSUPPORTED, "%s: 2^24 tiles of 128 x 128 or more", what);
   const bool some = rows > 0 && cols > 0;
   if ((e = check_rows(x, ld, cols, x_dtype == FP4_IN_FP32 ? 4 : 2, some, what, "x")) != FP4_OK) return e;
@@ -1044,7 +1042,8 @@ fp4_status fp8_gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f
   if ((e = check_f8_scale(scale, what)) != FP4_OK) return e;
   if (f % 128) return fail(FP4_EUNSUPPORTED, "%s: f must be a multiple of 128 (got %lld)", what, (long long)f);
   if (lddh > MAX_WIDTH || ldgu > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: lddh and ldgu must be at most 2^22", what);
-  if (((rows + 127) / 128) * (f / 128) >= MAX_F8_TILES) return fail(FP4_EUNSUPPORTED, "%s: 2^24 tiles or more", what);
+  if (!fp4k::f8_gated_grad_fits(rows, f, a.f32))
+    return fail(FP4_EUNSUPPORTED, "%s: 2^%d tiles of 128 x 128 or more", what, a.f32 ? 23 : 24);
   if (rows > 0 && f > 0) {
     if (!q && !qt) return fail(FP4_EINVAL, "%s: no view to write", what);
     if (q && (e = check_f8_out(q, s, scale, what, "row view")) != FP4_OK) return e;

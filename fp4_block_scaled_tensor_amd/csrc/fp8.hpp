@@ -23,6 +23,7 @@ struct F8QuantArgs {
   void* st;
   hipStream_t stream;
 };
+bool f8_quantize_fits(int64_t rows, int64_t cols);   // its tiles are no more than one launch holds
 hipError_t run_f8_quantize(const F8QuantArgs& a);
 
 struct F8Operand {
@@ -50,6 +51,7 @@ struct GatedGradArgs {
   void* st;
   hipStream_t stream;
 };
+bool f8_gated_grad_fits(int64_t rows, int64_t f, bool f32);   // the quantized form's tiles are no more than one launch holds
 hipError_t run_gated_grad(const GatedGradArgs& a);
 
 // y = x . W^T over one weight or over rows in expert order; gated: h = act(x . Wg^T) * (x . Wu^T).

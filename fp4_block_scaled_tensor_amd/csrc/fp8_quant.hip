@@ -28,7 +28,7 @@ struct Shape {
 using QuantShape = Shape<8, 2>;
 // The gated gradient, us with 8 rows, two waves / 4 rows, four / 4 rows, three: 8192 x 14336 bf16 297 / 309 / 412,
 // 2047 x 14336 float32 158 / 173 / 132.
-template <bool F32, int ACT>
+template <bool F32>
 using GradShape = std::conditional_t<F32, Shape<4, 3>, Shape<8, 2>>;
 
 struct Tile {
@@ -275,8 +275,8 @@ __device__ __forceinline__ void gated_grad1(float dh, float g, float u, float& d
 }
 
 template <int VIEW, int ACT, bool F32, int LOAD, bool E8>
-__global__ __launch_bounds__((GradShape<F32, ACT>::THREADS), (GradShape<F32, ACT>::OCC)) void k_f8_gated_grad(GradParams p) {
-  using S = GradShape<F32, ACT>;
+__global__ __launch_bounds__(GradShape<F32>::THREADS, GradShape<F32>::OCC) void k_f8_gated_grad(GradParams p) {
+  using S = GradShape<F32>;
   constexpr int P = S::P, ES = F32 ? 4 : 2;
   __shared__ Lds<S> lds;
   const int64_t br = blockIdx.x / p.tiles_c, bc = blockIdx.x - br * p.tiles_c;
@@ -420,6 +420,9 @@ __global__ __launch_bounds__(THREADS) void k_f8_dequantize(DequantParams p) {
 
 int64_t blocks(int64_t n) { return div_up(n, F8_BLOCK); }
 
+// whether a launch of one workgroup to a tile holds fewer than 2^32 threads (what is more is cut off without an error)
+bool tiles_fit(int64_t rows, int64_t cols, int threads) { return blocks(rows) * blocks(cols) < (int64_t(1) << 32) / threads; }
+
 // calls f with std::true_type or std::false_type
 template <class F>
 void with_bool(bool b, F f) {
@@ -460,6 +463,12 @@ TileOut tile_out(int64_t rows, int64_t cols, bool grid, uint8_t* q, void* s, uin
 }
 
 }  // namespace
+
+bool f8_quantize_fits(int64_t rows, int64_t cols) { return tiles_fit(rows, cols, QuantShape::THREADS); }
+
+bool f8_gated_grad_fits(int64_t rows, int64_t f, bool f32) {
+  return tiles_fit(rows, f, f32 ? GradShape<true>::THREADS : GradShape<false>::THREADS);
+}
 
 hipError_t run_f8_quantize(const F8QuantArgs& a) {
   if (a.rows == 0 || a.cols == 0) return hipSuccess;
@@ -518,7 +527,7 @@ hipError_t run_gated_grad(const GatedGradArgs& a) {
             constexpr int A = decltype(act)::value, LOAD = decltype(vec)::value ? LOAD_ALIGNED : LOAD_ROWS;
             constexpr bool F32 = decltype(f32)::value;
             k_f8_gated_grad<decltype(v)::value, A, F32, LOAD, decltype(e8)::value>
-                <<<grid, GradShape<F32, A>::THREADS, 0, a.stream>>>(p);
+                <<<grid, GradShape<F32>::THREADS, 0, a.stream>>>(p);
           });
         });
       });

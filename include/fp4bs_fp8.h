@@ -116,7 +116,8 @@ fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_expe
  *        dgu may be gu itself (same stride)
  * fp8_gated_grad - the same as operands of the next products: q, s the row view [rows x 2 f] with 1D
  * scales (dx = dgu . W), qt, st the transposed one [2 f x rows] (dW = dgu^T . x). Either pair may be
- * NULL. f must be a multiple of 128 (pad gate and up each with zero rows), lddh and ldgu at most 2^22.
+ * NULL. f must be a multiple of 128 (pad gate and up each with zero rows), lddh and ldgu at most 2^22; fewer
+ * than 2^24 tiles of 128 x 128 of dh, 2^23 for float32.
  */
 fp4_status gated_grad(const void* dh, int32_t dtype, int64_t rows, int64_t f, int64_t lddh, const void* gu,
                       int64_t ldgu, int32_t act, void* dgu, int64_t lddgu, void* stream);

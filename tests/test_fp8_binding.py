@@ -1,9 +1,11 @@
 """The 8-bit operators' binding on the host: operands by keyword, and what may be an operand (no GPU needed)."""
+import ctypes
+
 import pytest
 import torch
 
 import fp4_block_scaled_tensor_amd as fp4
-from fp4_block_scaled_tensor_amd import fp8
+from fp4_block_scaled_tensor_amd import _lib, fp8
 
 
 def host_operand(rows=4, k=128):
@@ -50,3 +52,14 @@ def test_codes_of_another_type_are_refused(dtype):
 def test_codes_of_the_right_types(dtype):
     q = torch.zeros(4, 256, dtype=torch.uint8).view(dtype)
     assert fp8._operand(fp4.F8Tensor(q, torch.zeros(4, 2), fp4.FP4_SCALES_1D, 4, 200), "a", torch.device("cpu")).rows == 4
+
+
+def test_gated_grad_tiles_of_a_launch():
+    """A launch holds fewer than 2^32 threads: 2^23 tiles of 128 x 128 are one too many for the float32 form's
+    workgroups of 512, 2^24 for the bf16 form's of 256."""
+    lib, p = _lib.load(), ctypes.c_void_p(4096)
+
+    def views(dtype, rows, f):
+        return lib.fp8_gated_grad(p, dtype, rows, f, f, p, 2 * f, 0, 0, p, p, p, p, None)
+    assert views(1, 1 << 16, 1 << 21) == _lib.FP4_EUNSUPPORTED and "tiles" in lib.fp4_last_error().decode()
+    assert views(0, 1 << 17, 1 << 21) == _lib.FP4_EUNSUPPORTED and "tiles" in lib.fp4_last_error().decode()
