@@ -329,8 +329,8 @@ fp4_status check_f8_operand(const fp8_operand* o, bool pointers, const char* wha
   if (o->layout < FP4_SCALES_1D || o->layout > FP4_SCALES_2D_T)
     return fail(FP4_EINVAL, "%s: %s: unknown scale layout %d", what, name, o->layout);
   if (o->rows < 0 || o->k < 0) return fail(FP4_EINVAL, "%s: %s: negative size", what, name);
-  if (o->rows > MAX_SLOTS) return fail(FP4_EUNSUPPORTED, "%s: %s: rows must be below 2^31", what, name);
-  if (o->k > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: %s: k must be at most 2^22", what, name);
+  if (o->rows > MAX_SLOTS || o->k > MAX_SLOTS)
+    return fail(FP4_EUNSUPPORTED, "%s: %s: rows and k must be below 2^31", what, name);
   if (pointers && o->rows > 0 && o->k > 0) return check_f8_out(o->q, o->s, o->scale, what, name);
   return FP4_OK;
 }
@@ -345,6 +345,7 @@ fp4_status check_f8_product(const fp8_operand* x, const fp8_operand* w, int32_t 
   fp4_status st;
   if ((st = check_f8_operand(x, pointers, what, "first operand")) != FP4_OK) return st;
   if ((st = check_f8_operand(w, pointers, what, "second operand")) != FP4_OK) return st;
+  if (x->k > MAX_WIDTH || w->k > MAX_WIDTH) return fail(FP4_EUNSUPPORTED, "%s: k must be at most 2^22", what);
   if (x->layout != FP4_SCALES_1D) return fail(FP4_EUNSUPPORTED, "%s: the first operand needs 1D scales", what);
   if (x->k != w->k)
     return fail(FP4_EINVAL, "%s: operands have different k (%lld vs %lld)", what, (long long)x->k, (long long)w->k);

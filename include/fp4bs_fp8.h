@@ -63,7 +63,7 @@ typedef struct {
 fp4_status fp8_quantize(const void* x, int32_t x_dtype, int64_t rows, int64_t cols, int64_t ld, int32_t view,
                         int32_t scale, uint8_t* q, void* s, uint8_t* qt, void* st, void* stream);
 
-/* fp8_dequantize - y [rows x k] = code * S (float32 product), row stride ldy, rounded to y_dtype. */
+/* fp8_dequantize - y [rows x k] = code * S (float32 product), row stride ldy, rounded to y_dtype. Rows and k below 2^31. */
 fp4_status fp8_dequantize(const fp8_operand* a, void* y, int32_t y_dtype, int64_t ldy, void* stream);
 
 /*

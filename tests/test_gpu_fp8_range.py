@@ -39,3 +39,20 @@ def test_fp8_gated_grad_of_the_largest_projections(scale):
         q, s = R.quantize_rows(v.cpu(), scale)
         assert torch.equal(t.q.cpu().view(torch.uint8), q)
         assert torch.equal(t.s.cpu() if scale == "f32" else t.s.cpu().view(torch.uint8), s)
+
+
+@pytest.mark.parametrize("scale", list(R.SCALES))
+def test_dequantize_of_a_long_transposed_operand(scale):
+    """fp8_quantize's transposed view of more than 2^22 rows is an operand of more than 2^22 columns: too long for a
+    product, not for its values."""
+    rows = (1 << 22) + 200
+    x = torch.randn(rows, 3, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+    t = fp4.fp8_quantize(x, fp4.COL, R.SCALES[scale])
+    assert (t.rows, t.k) == (3, rows)
+    v = fp4.fp8_dequantize(t)
+    last = rows // 128 * 128
+    for at in (slice(0, 256), slice(last - 256, rows)):   # whole blocks
+        q, s = R.quantize_rows(x[at].t().contiguous().cpu(), scale)
+        assert torch.equal(v[:, at].cpu(), R.values(q, s, "1d", 3, x[at].shape[0]).float())
+    with pytest.raises(fp4.FP4Error, match="k must be at most"):
+        fp4.fp8_gemm(t, t)
