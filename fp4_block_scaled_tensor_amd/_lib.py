@@ -103,8 +103,8 @@ EXPERTS_SIGNATURES = {
 
 # include/fp4bs_fp8.h
 FP8_EXPORTED = [
-    "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_expert_gemm", "fp8_gated", "fp8_gemm_workspace", "gated_grad",
-    "fp8_gated_grad",
+    "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_expert_gemm", "fp8_gated", "fp8_gemm_workspace", "fp8_gemm_form",
+    "gated_grad", "fp8_gated_grad",
 ]
 
 _F8 = ctypes.POINTER(F8Operand)
@@ -115,6 +115,7 @@ FP8_SIGNATURES = {
     "fp8_expert_gemm": ([_F8, _F8, _I32, _P, _P, _I32, _I64, _P, _SZ, _P], ctypes.c_int),
     "fp8_gated": ([_F8, _F8, _I32, _P, _I32, _P, _I32, _I64, _P, _P, _I32, _I64, _P, _SZ, _P], ctypes.c_int),
     "fp8_gemm_workspace": ([_I64, _F8, _I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "fp8_gemm_form": ([_I64, _F8, _I32, _I32, _I32, ctypes.POINTER(_I32)], ctypes.c_int),
     "gated_grad": ([_P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _P, _I64, _P], ctypes.c_int),
     "fp8_gated_grad": ([_P, _I32, _I64, _I64, _I64, _P, _I64, _I32, _I32, _P, _P, _P, _P, _P], ctypes.c_int),
 }

@@ -956,20 +956,35 @@ fp4_status fp8_dequantize(const fp8_operand* o, void* y, int32_t y_dtype, int64_
   return hip_status(fp4k::run_f8_dequantize(f8_operand(o), y, f32, ldy, (hipStream_t)stream), what);
 }
 
-fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
-                              size_t* ws_bytes) {
-  const char* what = "fp8_gemm_workspace";
+// Sizes alone, as fp8_gemm_workspace and fp8_gemm_form take them.
+static fp4_status f8_sizes(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
+                           const char* what, fp4k::F8GemmArgs& a) {
   if (gated < 0 || gated > 2) return fail(FP4_EINVAL, "%s: gated must be 0, 1 or 2", what);
   if (f32 != 0 && f32 != 1) return fail(FP4_EINVAL, "%s: f32 must be 0 or 1", what);
   if (!w) return fail(FP4_EINVAL, "%s: NULL weight", what);
-  if (!ws_bytes) return fail(FP4_EINVAL, "NULL size output");
   const fp8_operand x{nullptr, nullptr, w->scale, FP4_SCALES_1D, rows, w->k};
-  fp4k::F8GemmArgs a{};
   a.f32 = f32 != 0;
   a.codes = gated == 2;
-  fp4_status st = check_f8_product(&x, w, n_experts, gated != 0, false, what, a);
+  return check_f8_product(&x, w, n_experts, gated != 0, false, what, a);
+}
+
+fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
+                              size_t* ws_bytes) {
+  fp4k::F8GemmArgs a{};
+  fp4_status st = f8_sizes(rows, w, n_experts, gated, f32, "fp8_gemm_workspace", a);
   if (st != FP4_OK) return st;
+  if (!ws_bytes) return fail(FP4_EINVAL, "NULL size output");
   *ws_bytes = fp4k::f8_gemm_ws(a);
+  return ok();
+}
+
+fp4_status fp8_gemm_form(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
+                         int32_t* form) {
+  fp4k::F8GemmArgs a{};
+  fp4_status st = f8_sizes(rows, w, n_experts, gated, f32, "fp8_gemm_form", a);
+  if (st != FP4_OK) return st;
+  if (!form) return fail(FP4_EINVAL, "fp8_gemm_form: NULL form");
+  fp4k::f8_gemm_form(a, form);
   return ok();
 }
 

@@ -76,6 +76,7 @@ struct F8GemmArgs {
 };
 bool f8_gemm_fits(const F8GemmArgs& a);      // its tiles are no more than one launch holds (sizes alone)
 size_t f8_gemm_ws(const F8GemmArgs& a);      // bytes of F8GemmArgs::ws (sizes alone)
+void f8_gemm_form(const F8GemmArgs& a, int32_t form[4]);   // fp8_gemm_form of fp4bs_fp8.h (sizes alone)
 hipError_t run_f8_gemm(const F8GemmArgs& a);
 
 // ---- E4M3 blocks ----

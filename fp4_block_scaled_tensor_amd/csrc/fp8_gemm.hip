@@ -940,6 +940,16 @@ size_t f8_gemm_ws(const F8GemmArgs& a) {
   return turn.x + turn.w + (in_parts(a, t) ? (size_t)t.slices * a.x.rows * a.w.rows * 4 : 0);
 }
 
+void f8_gemm_form(const F8GemmArgs& a, int32_t form[4]) {
+  const bool some = a.x.rows > 0 && a.w.rows > 0;
+  const TilePlan t = some ? plan_tiles(a) : TilePlan{};
+  const Turned turn = some ? turned(a, t) : Turned{};
+  form[0] = t.bm;
+  form[1] = t.bn;
+  form[2] = t.slices;
+  form[3] = (turn.x ? 1 : 0) | (turn.w ? 2 : 0);
+}
+
 hipError_t run_f8_gemm(const F8GemmArgs& a) {
   if (a.x.rows == 0 || a.w.rows == 0) return hipSuccess;
   F8Params p{};

@@ -109,6 +109,11 @@ fp4_status fp8_gated(const fp8_operand* x, const fp8_operand* w, int32_t n_exper
  * or gu is float32), from rows of x and w's sizes: w's pointers are not looked at. */
 fp4_status fp8_gemm_workspace(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
                               size_t* ws_bytes);
+/* How those calls run on the current device, from the same sizes, for tests and profiles: form[0] rows of an
+ * output tile (0: the form for few rows, or nothing to do), form[1] its columns, form[2] the parts that K is split
+ * into, form[3] whose scales are copied turned first (1: x's, 2: w's, 3: both). */
+fp4_status fp8_gemm_form(int64_t rows, const fp8_operand* w, int32_t n_experts, int32_t gated, int32_t f32,
+                         int32_t* form);
 
 /*
  * gated_grad - dgu[m][j] = dh u act'(g), dgu[m][f + j] = dh act(g) in float32, rounded once.

@@ -1,0 +1,93 @@
+"""Every form of the 8-bit products (tests/_fp8_forms.py), exact on integers: sums below 2^24 of their unit, which both
+matrix cores and any order of adding give exactly."""
+import pytest
+import torch
+
+import fp4_block_scaled_tensor_amd as fp4
+from tests import _fp8 as R
+from tests import _fp8_forms as F
+
+pytestmark = pytest.mark.gpu
+
+
+def integers(rows, k, seed, layout, scale, least=-1):
+    """An operand of integers -3 .. 3 with scales 2^least .. 2^(least + 2), and its float64 values, on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.zeros(rows, R.blocks(k) * R.B, device="cuda")
+    q[:, :k] = torch.randint(-3, 4, (rows, k), generator=g, device="cuda").float()
+    shape = (rows, R.blocks(k)) if layout == "1d" else (R.blocks(rows), R.blocks(k)) if layout == "2d" else (R.blocks(k), R.blocks(rows))
+    e = torch.randint(least, least + 3, shape, generator=g, device="cuda")
+    # (a table: the GPU's float64 power is off by a unit for some of these exponents)
+    s = torch.tensor([2.0 ** (least + i) for i in range(3)], dtype=torch.float64, device="cuda")[e - least]
+    held = (e + 127).to(torch.uint8) if scale == "e8m0" else s.float()
+    if layout == "2dT":
+        s = s.t()
+    if layout != "1d":
+        s = s.repeat_interleave(R.B, dim=0)[:rows]
+    return fp4.F8Tensor(q.to(R.F8), held, R.LAYOUTS[layout], rows, k), q[:, :k].double() * s.repeat_interleave(R.B, dim=1)[:, :k]
+
+
+def layouts(size):
+    """All of them; of large weights one, and both kinds where the weight's scales may be turned too."""
+    m, n, k, e = size
+    if m * n * k < 2e10:
+        return list(R.LAYOUTS)
+    return ["1d", "2d"] if F.form(m, n, k, e, 0, 0)[3] else ["2d"]
+
+
+def operands(size, layout, scale, least=-1):
+    """x, the weight or stack, the first positions of the experts' rows (None: one weight), the product in float64."""
+    m, n, k, e = size
+    x, xv = integers(m, k, 1, layout="1d", scale=scale, least=least)
+    if not e:
+        w, wv = integers(n, k, 2, layout, scale)
+        return x, w, None, xv @ wv.t().contiguous()
+    share = torch.tensor([(1, 0, 3, 2, 7)[i % 5] for i in range(e)], dtype=torch.float64)
+    ends = (share.cumsum(0) / share.sum() * (m - m // 16)).long()   # a sixteenth of the rows is dropped
+    offsets = torch.cat([torch.zeros(1, dtype=torch.long), ends])
+    each, y = [], torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    for i in range(e):
+        t, wv = integers(n, k, 10 + i, layout, scale)
+        each.append(t)
+        lo, hi = int(offsets[i]), int(offsets[i + 1])
+        if hi > lo:
+            y[lo:hi] = xv[lo:hi] @ wv.t().contiguous()
+    return x, fp4.fp8_stack(each), offsets.to(torch.int32).cuda(), y
+
+
+def name(size):
+    return "x".join(map(str, size))
+
+
+@pytest.mark.parametrize("scale", list(R.SCALES))
+@pytest.mark.parametrize("size", F.GEMM, ids=name)
+def test_product(size, scale):
+    for layout in layouts(size):
+        x, w, offsets, y64 = operands(size, layout, scale)
+        want = y64.float()
+        assert torch.equal(want.double(), y64)
+        for dtype in (torch.bfloat16, torch.float32):
+            got = fp4.fp8_gemm(x, w, dtype) if offsets is None else fp4.fp8_expert_gemm(x, w, offsets, dtype)
+            assert torch.equal(got, want.to(dtype)), (layout, dtype)
+
+
+@pytest.mark.parametrize("scale", list(R.SCALES))
+@pytest.mark.parametrize("size", F.GATED, ids=name)
+def test_gated(size, scale):
+    """The projections exact, h against float64 within the activation's arithmetic, and h in bf16 and as codes what
+    rounding or quantizing the float32 h gives."""
+    for layout in layouts(size):
+        x, w, offsets, gu64 = operands(size, layout, scale, least=-5)   # gates of a few units
+        f = gu64.shape[1] // 2
+        h, gu = fp4.fp8_gated(x, w, "silu", torch.float32, save=torch.float32, plan=offsets)
+        assert torch.equal(gu.double(), gu64), layout
+        g, u = gu64[:, :f], gu64[:, f:]
+        h64 = g * torch.sigmoid(g) * u
+        assert ((h.double() - h64).abs() <= 2.0 ** -20 * (1 + g.abs()) * u.abs() + 2.0 ** -24 * h64.abs()).all(), layout
+        del h64, g, u
+        q, gb = fp4.fp8_gated(x, w, "silu", torch.float8_e4m3fn, save=torch.bfloat16, plan=offsets)
+        assert torch.equal(gb, gu.to(torch.bfloat16)), layout
+        want = fp4.fp8_quantize(h, fp4.ROW, R.SCALES[scale])
+        assert torch.equal(q.q.view(torch.uint8), want.q.view(torch.uint8)), layout
+        assert torch.equal(q.s.view(torch.uint8), want.s.view(torch.uint8)), layout
+        assert torch.equal(fp4.fp8_gated(x, w, "silu", plan=offsets)[0], h.to(torch.bfloat16)), layout
