@@ -13,7 +13,7 @@ GEMM = [(17, 28672, 4096, 0), (2047, 4096, 14336, 0), (1, 70, 128, 0), (17, 70, 
         (4100, 70, 32768, 8), (6144, 1030, 14336, 32)]
 GATED = [(4, 28672, 4096, 0), (8192, 28672, 4096, 0), (1, 70, 128, 0), (17, 70, 1100, 0), (4100, 520, 128, 0), (17, 70, 2048, 0),
          (6144, 70, 4096, 0), (6144, 520, 128, 0), (8191, 1030, 128, 0), (129, 2050, 32768, 0), (6144, 200, 2048, 0),
-         (4100, 520, 8191, 0), (515, 200, 4096, 0),
+         (4100, 520, 8191, 0), (515, 200, 4096, 0), (129, 200, 300, 0),
          (1, 70, 128, 3), (17, 70, 128, 3), (17, 70, 2048, 3), (8191, 200, 128, 3), (6144, 520, 128, 3), (2047, 200, 2048, 3),
          (6144, 70, 4096, 3), (2100, 3584, 128, 8), (400, 2050, 14336, 3), (4100, 200, 128, 3), (4100, 70, 32768, 8),
          (1000, 200, 2048, 3), (6144, 1030, 14336, 32)]
@@ -28,8 +28,8 @@ def form(m, n, k, experts, gated, f32, layout=1):
 
 
 def forms(size, gated):
-    """What a size takes in each of its calls: (experts, h as codes, float32 output, rows, columns, split, turned)."""
-    calls = [(1, 0), (1, 1), (2, 0)] if gated else [(0, 0), (0, 1)]
+    """What a size takes in each of its calls: (experts, h as codes, a float32 output, rows, columns, split, turned)."""
+    calls = [(1, 0), (1, 1), (2, 0), (2, 1)] if gated else [(0, 0), (0, 1)]
     out = set()
     for g, f32 in calls:
         bm, bn, parts, turned = form(*size, g, f32)

@@ -85,9 +85,29 @@ def test_gated(size, scale):
         h64 = g * torch.sigmoid(g) * u
         assert ((h.double() - h64).abs() <= 2.0 ** -20 * (1 + g.abs()) * u.abs() + 2.0 ** -24 * h64.abs()).all(), layout
         del h64, g, u
-        q, gb = fp4.fp8_gated(x, w, "silu", torch.float8_e4m3fn, save=torch.bfloat16, plan=offsets)
-        assert torch.equal(gb, gu.to(torch.bfloat16)), layout
         want = fp4.fp8_quantize(h, fp4.ROW, R.SCALES[scale])
-        assert torch.equal(q.q.view(torch.uint8), want.q.view(torch.uint8)), layout
-        assert torch.equal(q.s.view(torch.uint8), want.s.view(torch.uint8)), layout
+        for kept in (torch.bfloat16, torch.float32):
+            q, gk = fp4.fp8_gated(x, w, "silu", torch.float8_e4m3fn, save=kept, plan=offsets)
+            assert torch.equal(gk, gu.to(kept)), (layout, kept)
+            assert torch.equal(q.q.view(torch.uint8), want.q.view(torch.uint8)), (layout, kept)
+            assert torch.equal(q.s.view(torch.uint8), want.s.view(torch.uint8)), (layout, kept)
         assert torch.equal(fp4.fp8_gated(x, w, "silu", plan=offsets)[0], h.to(torch.bfloat16)), layout
+
+
+@pytest.mark.parametrize("scale", list(R.SCALES))
+@pytest.mark.parametrize("size", [(3, 72, 300, 0), (9, 150, 640, 5), (70, 200, 1100, 0), (200, 528, 2048, 3), (700, 1040, 384, 0)], ids=name)
+def test_gated_in_every_pair_of_types(size, scale):
+    """h in each type, the projections in each or not kept, and each activation: all one result, rounded."""
+    x, w, offsets, gu64 = operands(size, "2d", scale, least=-5)
+    for act in ("silu", "gelu", "gelu_tanh"):
+        h32, _ = fp4.fp8_gated(x, w, act, torch.float32, save=torch.float32, plan=offsets)
+        codes = fp4.fp8_quantize(h32, fp4.ROW, R.SCALES[scale])
+        for out in (torch.bfloat16, torch.float32, torch.float8_e4m3fn):
+            for kept in (None, torch.bfloat16, torch.float32):
+                h, gu = fp4.fp8_gated(x, w, act, out, save=kept, plan=offsets)
+                assert gu is None if kept is None else torch.equal(gu, gu64.to(kept)), (act, out, kept)
+                if out is torch.float8_e4m3fn:
+                    assert torch.equal(h.q.view(torch.uint8), codes.q.view(torch.uint8)), (act, kept)
+                    assert torch.equal(h.s.view(torch.uint8), codes.s.view(torch.uint8)), (act, kept)
+                else:
+                    assert torch.equal(h, h32.to(out)), (act, out, kept)
