@@ -360,7 +360,7 @@ fp4_status check_f8_product(const fp8_operand* x, const fp8_operand* w, int32_t 
   a.n_experts = n_experts ? n_experts : 1;
   a.offsets_given = n_experts != 0;
   a.gated = gated;
-  if (!fp4k::f8_gemm_fits(a)) return fail(FP4_EUNSUPPORTED, "%s: 2^23 output tiles or more", what);
+  if (!fp4k::f8_gemm_fits(a)) return fail(FP4_EUNSUPPORTED, "%s: more output tiles than a launch of 2^32 threads holds", what);
   return FP4_OK;
 }
 

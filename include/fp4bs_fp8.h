@@ -98,8 +98,9 @@ fp4_status fp8_dequantize(const fp8_operand* a, void* y, int32_t y_dtype, int64_
  * act and the product are taken in float32 on the unrounded projections, whose sums are those of a
  * float32 y above where h or gu is float32, and those of a bf16 y otherwise.
  *
- * Calls whose output tiles (of at least 32 x 128, and one more row of tiles to an expert) are 2^23
- * or more return FP4_EUNSUPPORTED.
+ * A launch holds fewer than 2^32 threads: calls of 2^23 or more tiles of 128 or 256 rows, or of 2^24 or more lower
+ * ones, return FP4_EUNSUPPORTED (fp8_gemm_form gives the tiles; an expert counts one more row of them). Fewer than
+ * 2^22 tiles of 32 x 128 are always accepted.
  */
 fp4_status fp8_gemm(const fp8_operand* a, const fp8_operand* b, void* y, int32_t y_dtype, int64_t ldy, void* ws,
                     size_t ws_bytes, void* stream);

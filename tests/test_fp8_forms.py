@@ -43,3 +43,28 @@ def test_form_refuses():
     assert lib.fp8_gemm_form(4, w(rows=63), 0, 1, 0, f) == _lib.FP4_EINVAL
     assert lib.fp8_gemm_form(4, w(), 1025, 0, 0, f) == _lib.FP4_EUNSUPPORTED
     assert lib.fp8_gemm_form(0, w(), 0, 0, 0, f) == _lib.FP4_OK and tuple(f) == (0, 0, 0, 0)
+
+
+def status(m, n, k, experts=0, gated=0, f32=0):
+    f = (ctypes.c_int32 * 4)()
+    w = _lib.F8Operand(None, None, _lib.FP8_SCALE_E8M0, _lib.FP4_SCALES_2D, n, k)
+    st = _lib.load().fp8_gemm_form(m, ctypes.byref(w), experts, gated, f32, f)
+    return st, tuple(f)
+
+
+@pytest.mark.parametrize("f32", [0, 1])
+@pytest.mark.parametrize("n,k", [(64, 128), (200, 128), (256, 256), (4096, 512), (100000, 128)])
+def test_the_largest_launches(n, k, f32):
+    """What is accepted has fewer than 2^32 threads, by the tiles that the call says it takes; what is refused is past
+    the tiles that are always accepted, and says why."""
+    div = lambda a, b: -(-a // b)   # noqa: E731
+    for log in range(20, 31):
+        for m in (1 << log, (1 << log) + (1 << log - 1), (1 << log + 1) - 1):
+            st, (bm, bn, parts, _) = status(m, n, k, f32=f32)
+            if st == _lib.FP4_OK:
+                assert div(m, bm) * div(n, bn) * parts * (512 if bm >= 128 else 256) < 1 << 32, m
+            else:
+                assert st == _lib.FP4_EUNSUPPORTED and "tiles" in _lib.load().fp4_last_error().decode()
+                assert div(m, 32) * div(n, 128) >= 1 << 22, m
+    for e in (1, 1024):
+        assert status(1 << 20, 256, k, experts=e, f32=f32)[0] == _lib.FP4_OK
