@@ -138,8 +138,9 @@ __device__ __forceinline__ F8Scale hs_scale(const F8Params& p, uint32_t amax) {
 // two operands' rows of one block of K, and their scales, are copied straight into LDS, two blocks deep. Row r
 // (128 bytes) keeps its 16-byte piece j at j ^ ((r >> 1) & 7), so that 16 rows reading one piece fall on all banks.
 //
-// Tall tiles are bound by the matrix cores, at 58% of their cycles for 256 rows: a block takes 1.43 to 1.6 us
-// against 1.02 of its products alone; without its copies it takes 1.26. 8192 x 4096 -> 14336 380 us with E8M0
+// Tall tiles are bound by the matrix cores, busy for 61% of the cycles of 8192 x 4096 -> 14336 (44 to 52% where
+// float32 scales, experts' last tiles or a gated product's outputs add to them): a block takes 1.43 to 1.6 us against
+// 1.02 of its products alone; without its copies it takes 1.26. 8192 x 4096 -> 14336 380 us with E8M0
 // scales (2.5 PFLOP/s), 455 with float32 ones, whose multiply-adds are the vector unit's; widened codes 1.1 PFLOP/s.
 // Low tiles are bound by the weight's bytes and a block's latency (17 x 4096 -> 28672 31 us, 3.8 TB/s).
 constexpr int ROWB = F8_BLOCK;

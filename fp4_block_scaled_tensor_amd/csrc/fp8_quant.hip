@@ -295,7 +295,7 @@ __global__ __launch_bounds__(GradShape<F32>::THREADS, GradShape<F32>::OCC) void 
   TileOut o = p.out;
   o.row0 = o.tcol0 = t.r0;
   // The gate's half, then the up projection's from the inputs anew: both at once take the registers of the other
-  // workgroups whose loads would go on meanwhile (8192 x 14336 bf16 457 us at best, 292 so: 4.0 TB/s, bound by the
+  // workgroups whose loads would go on meanwhile (8192 x 14336 bf16 457 us at best, 296 so: 4.0 TB/s, bound by the
   // activation's and the quantizer's vector work beside the loads). The words are opaque in between, or the
   // compiler keeps what the halves share.
 #pragma unroll
