@@ -1,11 +1,15 @@
 """Every form of the 8-bit products (tests/_fp8_forms.py), exact on integers: sums below 2^24 of their unit, which both
 matrix cores and any order of adding give exactly."""
+import ctypes
+
 import pytest
 import torch
 
 import fp4_block_scaled_tensor_amd as fp4
+from fp4_block_scaled_tensor_amd import _lib
 from tests import _fp8 as R
 from tests import _fp8_forms as F
+from tests.test_gpu_fp8_usage import Guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +115,34 @@ def test_gated_in_every_pair_of_types(size, scale):
                     assert torch.equal(h.s.view(torch.uint8), codes.s.view(torch.uint8)), (act, kept)
                 else:
                     assert torch.equal(h, h32.to(out)), (act, out, kept)
+
+
+@pytest.mark.parametrize("scale", list(R.SCALES))
+@pytest.mark.parametrize("size,layout", [((17, 2050, 4096, 0), "2d"), ((2047, 200, 2048, 3), "2d"), ((4100, 70, 32768, 0), "1d"),
+                                         ((4100, 70, 32768, 8), "2d"), ((4100, 4096, 14336, 0), "1d"), ((6144, 1030, 14336, 8), "1d")])
+def test_workspaces_and_outputs_between_guards(size, layout, scale):
+    """Split sums, turned scales and both in one workspace of exactly the bytes that are asked for; outputs exact."""
+    m, n, k, e = size
+    x, w, offsets, y64 = operands(size, layout, scale, least=-5)
+    lib, nb, stream = _lib.load(), ctypes.c_size_t(), torch.cuda.current_stream().cuda_stream
+    ox, ow = (_lib.F8Operand(t.q.data_ptr(), t.s.data_ptr(), R.SCALES[scale], t.layout, t.rows, t.k) for t in (x, w))
+    off = None if offsets is None else offsets.data_ptr()
+    for dt, dtype in ((0, torch.bfloat16), (1, torch.float32)):
+        _lib.check(lib.fp8_gemm_workspace(m, ctypes.byref(ow), e, 0, dt, ctypes.byref(nb)))
+        ws, y = Guarded(max(16, nb.value)), Guarded(m * n * dtype.itemsize)
+        if e:
+            _lib.check(lib.fp8_expert_gemm(ctypes.byref(ox), ctypes.byref(ow), e, off, y.ptr(), dt, n, ws.ptr(), nb.value, stream))
+        else:
+            _lib.check(lib.fp8_gemm(ctypes.byref(ox), ctypes.byref(ow), y.ptr(), dt, n, ws.ptr(), nb.value, stream))
+        assert ws.intact() and y.intact()
+        assert torch.equal(y.get(dtype).view(m, n), y64.float().to(dtype))
+    kc = R.blocks(n // 2)
+    _lib.check(lib.fp8_gemm_workspace(m, ctypes.byref(ow), e, 2, 0, ctypes.byref(nb)))
+    ws, q, s = Guarded(max(16, nb.value)), Guarded(m * kc * R.B), Guarded(m * kc * (1 if scale == "e8m0" else 4))
+    gu = Guarded(m * n * 2)
+    _lib.check(lib.fp8_gated(ctypes.byref(ox), ctypes.byref(ow), e, off, 0, q.ptr(), _lib.FP8_OUT_E4M3, 0, s.ptr(), gu.ptr(), 0, n,
+                             ws.ptr(), nb.value, stream))
+    assert all(b.intact() for b in (ws, q, s, gu))
+    assert torch.equal(gu.get(torch.bfloat16).view(m, n), y64.float().to(torch.bfloat16))
+    codes = fp4.fp8_quantize(fp4.fp8_gated(x, w, "silu", torch.float32, plan=offsets)[0], fp4.ROW, R.SCALES[scale])
+    assert torch.equal(q.get(), codes.q.view(torch.uint8).flatten()) and torch.equal(s.get(), codes.s.view(torch.uint8).flatten())
