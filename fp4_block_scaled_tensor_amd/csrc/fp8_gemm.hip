@@ -38,13 +38,13 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p) {
 }
 
 // The copies of lds_copy.hpp for all lanes (mask -1) or, without a branch, for none (0). Only
-// in code that all 64 lanes of a wave execute.
+// in code that all 64 lanes of a wave execute. (Five wait states before the load, as there.)
 __device__ __forceinline__ void lds_dma16_masked(const void* sbase, uint32_t voff, uint32_t dst, int mask) {
   asm volatile(
       "s_mov_b32 m0, %2\n\t"
       "s_mov_b32 exec_lo, %3\n\t"
       "s_mov_b32 exec_hi, %3\n\t"
-      "s_nop 0\n\t"
+      "s_nop 1\n\t"
       "global_load_lds_dwordx4 %0, %1\n\t"
       "s_mov_b64 exec, -1"
       :
@@ -58,7 +58,7 @@ __device__ __forceinline__ void lds_dma_scale_masked(const void* sbase, uint32_t
         "s_mov_b32 m0, %2\n\t"
         "s_mov_b32 exec_lo, %3\n\t"
         "s_mov_b32 exec_hi, %3\n\t"
-        "s_nop 0\n\t"
+        "s_nop 1\n\t"
         "global_load_lds_ubyte %0, %1\n\t"
         "s_mov_b64 exec, -1"
         :
@@ -69,7 +69,7 @@ __device__ __forceinline__ void lds_dma_scale_masked(const void* sbase, uint32_t
         "s_mov_b32 m0, %2\n\t"
         "s_mov_b32 exec_lo, %3\n\t"
         "s_mov_b32 exec_hi, %3\n\t"
-        "s_nop 0\n\t"
+        "s_nop 1\n\t"
         "global_load_lds_dword %0, %1\n\t"
         "s_mov_b64 exec, -1"
         :
